@@ -1,7 +1,8 @@
 """Python binding of libmoe, the B200 quantized MoE expert step.
 
 Argument marshalling only: every function below forwards to the C ABI
-declared in include/moe.h with the same name; all arithmetic runs in the
+declared in include/moe.h (the training side: include/moe_train.h, bound in
+train.py) with the same name; all arithmetic runs in the
 CUDA kernels of libmoe.so.  There is no CPU fallback: if the shared library
 is missing, the first call raises.
 
@@ -15,6 +16,9 @@ import os
 from pathlib import Path
 
 from .layer import MoELayer, alloc_step_buffers  # noqa: F401
+from .train import (MOE_Q8, SIGNATURES as _TRAIN_SIGNATURES, TrainStep, moe_act_pack8, moe_act_unpack8,  # noqa: F401
+                    moe_balance_loss, moe_balance_ws_size, moe_expert_ffn_backward, moe_expert_ffn_backward_ws_size,
+                    moe_route_backward, moe_router_backward, moe_router_backward_ws_size)
 
 _PKG = Path(__file__).resolve().parent
 # MOE_LIBRARY=debug loads the MOE_DEBUG build (index checks report to the
@@ -22,6 +26,7 @@ _PKG = Path(__file__).resolve().parent
 LIB_PATH = _PKG / ("_build_debug" if os.environ.get("MOE_LIBRARY") == "debug" else "_build") / "libmoe.so"
 MOE_BUILD_DEBUG = 1
 HEADER = _PKG.parent / "include" / "moe.h"
+TRAIN_HEADER = _PKG.parent / "include" / "moe_train.h"
 
 MOE_OK, MOE_EINVAL, MOE_ENOMEM, MOE_ECUDA, MOE_EBUSY, MOE_ETIMEDOUT, MOE_EIO, MOE_EDEVICE = range(8)
 MOE_F32, MOE_BF16 = 0, 1
@@ -147,6 +152,7 @@ def lib():
         "devcache_stats": (I, [P, C.POINTER(DevCacheStats)]),
         "devcache_snapshot": (I, [P, P, P]),
     }
+    sig.update(_TRAIN_SIGNATURES)
     for name, (res, args) in sig.items():
         f = getattr(L, name)
         f.restype = res
