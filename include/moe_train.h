@@ -109,8 +109,7 @@ int moe_route_backward(const float *logits, const int32_t *topk_ids, const float
  *           weights, and each token's x and dy divided by a power of two of its
  *           own (undone in fp32 at the end), so that neither's scale matters;
  *           the gradients of g and u are rounded to fp16 between the two
- *           products.  fp32 accumulation.  At most 4095 groups (min(E, T*k) +
- *           shared), blobs in device memory.
+ *           products.  fp32 accumulation.  Blobs in device memory.
  *           MOE_MODE_AUTO: GEMV up to 16 tokens, else GEMM.
  *  Shapes as for moe_expert_ffn_*: H a multiple of 128 up to 8192, I up to 4096.
  *  ws: at least moe_expert_ffn_backward_ws_size(...) bytes. */

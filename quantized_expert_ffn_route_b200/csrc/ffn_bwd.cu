@@ -234,9 +234,14 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_columns(FfnBackward a, GemvB
 }
 
 // dx[t] = sum_j w[t,j] dxp[row(t,j)] + dxp[shared row t], in slot order, and
-// d_topk_w[t,j] = the sum of its row's shares.  One block per token.
-__global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, GemvBwdWs ws, int shares) {
+// d_topk_w[t,j] = the sum of its row's shares; with `scale`, times the token's
+// sx sd and sx sx sd.  One block per token.
+__global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, const float *__restrict__ dxp,
+                                                           const float *__restrict__ dwp, int shares,
+                                                           const uint8_t *__restrict__ ok,
+                                                           const float2 *__restrict__ scale) {
     const size_t t = blockIdx.x;
+    const float2 sc = scale ? scale[t] : make_float2(1.f, 1.f);
     __shared__ int row_s[32];
     __shared__ float w_s[32];
     const int j = threadIdx.x;
@@ -245,31 +250,33 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, GemvBw
         if (row < 0 || row >= a.T * a.k) {
             report(a.err, MOE_DEVERR_BAD_ROW);
             row = -1;
-        } else if (!ws.ok[row]) {
+        } else if (!ok[row]) {
             row = -1;
         }
         row_s[j] = row;
         w_s[j] = a.topk_w[t * a.k + j];
         float sum = 0.f;
         if (row >= 0)
-            for (int i = 0; i < shares; ++i) sum += ws.dwp[static_cast<size_t>(row) * shares + i];
-        a.d_topk_w[t * a.k + j] = sum;
+            for (int i = 0; i < shares; ++i) sum += dwp[static_cast<size_t>(row) * shares + i];
+        a.d_topk_w[t * a.k + j] = sum * sc.x * sc.y * sc.x;
     }
     __syncthreads();
     for (int h4 = threadIdx.x; h4 < a.H / 4; h4 += kBwThreads) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i = 0; i < a.k; ++i) {
             if (row_s[i] < 0) continue;
-            const float4 v = load4(ws.dxp + static_cast<size_t>(row_s[i]) * a.H + 4 * h4);
+            const float4 v = load4(dxp + static_cast<size_t>(row_s[i]) * a.H + 4 * h4);
             acc.x = fmaf(w_s[i], v.x, acc.x);
             acc.y = fmaf(w_s[i], v.y, acc.y);
             acc.z = fmaf(w_s[i], v.z, acc.z);
             acc.w = fmaf(w_s[i], v.w, acc.w);
         }
         if (a.shared) {
-            const float4 v = load4(ws.dxp + (static_cast<size_t>(a.T) * a.k + t) * a.H + 4 * h4);
+            const float4 v = load4(dxp + (static_cast<size_t>(a.T) * a.k + t) * a.H + 4 * h4);
             acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         }
+        acc.x = acc.x * sc.x * sc.y, acc.y = acc.y * sc.x * sc.y;
+        acc.z = acc.z * sc.x * sc.y, acc.w = acc.w * sc.x * sc.y;
         const size_t at = t * (a.H / 4) + h4;
         if (a.dx_dtype == MOE_BF16) {
             __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
@@ -324,9 +331,17 @@ static int launch_gemv_bwd(const FfnBackward &a, const GemvBwdWs &w, cudaStream_
                      "backward smem attribute");
     if (rc) return rc;
     k_bwd_columns<BITS, false><<<grid(a.H / kStrip), kBwThreads, columns(2 * a.I), s>>>(a, w);
-    k_bwd_gather<<<a.T, kBwThreads, 0, s>>>(a, w, a.I / kStrip);
-    count_launches(4);
-    return cuda_status(cudaGetLastError(), "expert backward launch");
+    count_launches(3);
+    rc = cuda_status(cudaGetLastError(), "expert backward launch");
+    if (rc) return rc;
+    return launch_ffn_backward_gather(a, w.dxp, w.dwp, a.I / kStrip, w.ok, nullptr, s);
+}
+
+int launch_ffn_backward_gather(const FfnBackward &a, const float *dxp, const float *dwp, int shares,
+                               const uint8_t *ok, const float2 *scale, cudaStream_t s) {
+    k_bwd_gather<<<a.T, kBwThreads, 0, s>>>(a, dxp, dwp, shares, ok, scale);
+    count_launches(1);
+    return cuda_status(cudaGetLastError(), "expert backward gather launch");
 }
 
 int launch_ffn_backward_gemv(const FfnBackward &a, void *ws, cudaStream_t s) {

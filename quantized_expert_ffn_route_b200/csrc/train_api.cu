@@ -95,14 +95,14 @@ int moe_route_backward(const float *logits, const int32_t *topk_ids, const float
 
 // ---------------------------------------------------------------- experts
 static int backward_mode(int mode, int T) {
-    if (mode == MOE_MODE_AUTO) return MOE_MODE_GEMV;
+    if (mode == MOE_MODE_AUTO) return T <= 16 ? MOE_MODE_GEMV : MOE_MODE_GEMM;
     return mode;
 }
 
 size_t moe_expert_ffn_backward_ws_size(int bits, int T, int k, int H, int I, int E, int mode) {
     if ((bits != 2 && bits != 4) || T <= 0 || k <= 0 || H <= 0 || I <= 0 || E <= 0) return 0;
     mode = backward_mode(mode, T);
-    return ffn_backward_gemv_ws_bytes(T, k, H, I);
+    return mode == MOE_MODE_GEMM ? ffn_backward_gemm_ws_bytes(T, k, H, I, E) : ffn_backward_gemv_ws_bytes(T, k, H, I);
 }
 
 int moe_expert_ffn_backward(int bits, const void *const *expert_blobs, const int32_t *expert_offsets,
@@ -131,6 +131,7 @@ int moe_expert_ffn_backward(int bits, const void *const *expert_blobs, const int
             "the buffers must be 16-byte aligned");
     REQUIRE(dx != dy && dx != x, "dx must not be x or dy");
     mode = backward_mode(mode, T);
+    REQUIRE(mode == MOE_MODE_GEMV || ffn_backward_gemm_supported(T, k, H, I, E), "too many tiles for GEMM mode");
     const size_t need = moe_expert_ffn_backward_ws_size(bits, T, k, H, I, E, mode);
     REQUIRE(ws && ws_bytes >= need && aligned16(ws), "workspace too small: need %zu bytes", need);
     unsigned *err = device_error_word();
@@ -145,7 +146,8 @@ int moe_expert_ffn_backward(int bits, const void *const *expert_blobs, const int
     a.bits = bits, a.x_dtype = x_dtype, a.dy_dtype = dy_dtype, a.dx_dtype = dx_dtype;
     a.T = T, a.k = k, a.H = H, a.I = I, a.E = E;
     a.err = err;
-    return launch_ffn_backward_gemv(a, ws, reinterpret_cast<cudaStream_t>(s));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(s);
+    return mode == MOE_MODE_GEMM ? launch_ffn_backward_gemm(a, ws, st) : launch_ffn_backward_gemv(a, ws, st);
 }
 
 // ----------------------------------------------------------------- router
