@@ -18,10 +18,10 @@
 // until the gather multiplies by w sx sd in fp32.
 //
 // One persistent block per SM.  Roles:
-//   dequantising warps read codes straight to registers, one step of 128 K
-//       values ahead, and write fp16 tiles to the A stages; the four lanes of
-//       a row read its 64 (4-bit) or 32 bytes, so that whole sectors are used
-//       and no shared memory is spent on codes;
+//   dequantising warps, two groups that take alternate stages, read codes
+//       straight to registers two of their stages ahead (no shared memory is
+//       spent on codes) and write fp16 tiles to the A stages, four blocks of 32
+//       a thread between two barriers;
 //   loader warps gather the rows (cp.async) into the B stages;
 //   one thread issues tcgen05.mma; four warps read the accumulators.
 // Every wait is bounded (MOE_DEVERR_TIMEOUT; all roles then leave their loops
@@ -66,26 +66,32 @@ struct TcArgs {
 template <int BITS, int PHASE, int MAXN_>
 struct Cfg {
     static constexpr int MAXN = MAXN_;
-    static constexpr int NM = PHASE == 1 ? 3 : 2;             // A tiles per stage: g, u, q, or two halves of 256 rows
-    static constexpr int NB = PHASE == 1 ? 2 : 1;             // B tiles per stage: x and dy, or [dg | du]
-    static constexpr int DEQ = PHASE == 1 ? 12 : 8;           // dequantising warps
+    // phase 1: a stage is 64 of K, three A tiles (g, u, q; an accumulator each)
+    // and two B tiles (x, dy); phase 2: 128 of K, two A and two B tiles of 64,
+    // one accumulator
+    static constexpr int NM = PHASE == 1 ? 3 : 2;
+    static constexpr int NB = 2;
+    static constexpr int ND = PHASE == 1 ? 3 : 1;
+    static constexpr int KSTAGE = PHASE == 1 ? kBK : 2 * kBK;
+    static constexpr int GROUP = PHASE == 1 ? 6 : 4;          // warps of a dequantising group: 4 blocks a thread
+    static constexpr int DEQ = 2 * GROUP;
+    static constexpr int EPI = 4;
     static constexpr int LOAD = 4;                            // loader warps
-    static constexpr int THREADS = 32 * (DEQ + 4 + 1 + LOAD);
+    static constexpr int THREADS = 32 * (DEQ + EPI + 1 + LOAD);
     static constexpr uint32_t A_STAGE = NM * kMat;
     static constexpr uint32_t B_TILE = MAXN * 128;
     static constexpr uint32_t B_STAGE = NB * B_TILE;
-    static constexpr int SA = PHASE == 1 ? (MAXN > 64 ? 2 : 3) : 3;
-    static constexpr int SB = PHASE == 1 ? (MAXN > 64 ? 3 : 4) : 3;
-    static constexpr int ACC = 2 * NM * MAXN <= 512 ? 2 : 1;  // accumulator sets
-    static constexpr int TMEM = ACC * NM * MAXN <= 256 ? 256 : 512;
+    static constexpr int SA = PHASE == 1 ? (MAXN > 64 ? 2 : 3) : (MAXN > 64 ? 3 : 4);
+    static constexpr int SB = PHASE == 1 ? (MAXN > 64 ? 3 : 4) : (MAXN > 64 ? 2 : 4);
+    static constexpr int ACC = 2 * ND * MAXN <= 512 ? 2 : 1;  // accumulator sets
+    static constexpr int TMEM = ACC * ND * MAXN <= 128 ? 128 : ACC * ND * MAXN <= 256 ? 256 : 512;
     static constexpr uint32_t OFF_B = SA * A_STAGE;
-    static constexpr uint32_t OFF_TOK = OFF_B + SB * B_STAGE;
-    static constexpr uint32_t OFF_SX = OFF_TOK + MAXN * 4;
-    static constexpr uint32_t OFF_BAR = (OFF_SX + (PHASE == 1 ? 4 * MAXN * 4 : 0) + 15) / 16 * 16;   // a copy per epilogue warp
+    static constexpr uint32_t OFF_SX = OFF_B + SB * B_STAGE;
+    static constexpr uint32_t OFF_BAR = OFF_SX + (PHASE == 1 ? EPI * MAXN * 4 : 0);   // a copy per epilogue warp
     static constexpr uint32_t SMEM = OFF_BAR + 24 * 8 + 16 + 1024;
     static_assert(SMEM <= kSmemMax, "shared memory per block");
     static_assert(2 * SA + 2 * SB + 5 <= 24, "barrier slots");
-    static_assert(ACC * NM * MAXN <= 512, "TMEM columns");
+    static_assert(ACC * ND * MAXN <= 512, "TMEM columns");
     static_assert(MAXN % (4 * LOAD) == 0 && MAXN % 16 == 0 && MAXN <= 256, "rows per loader warp");
 };
 
@@ -137,20 +143,20 @@ __device__ __forceinline__ void put_block(Codes<BITS> c, __half d, uint32_t row,
     }
 }
 
-__device__ __forceinline__ __half half_of(uint2 v, int i) {
-    const uint32_t w = i & 2 ? v.y : v.x;
-    return __ushort_as_half(static_cast<unsigned short>(i & 1 ? w >> 16 : w));
-}
+// What a dequantising thread reads for one stage: four blocks and their steps.
+template <int BITS> struct Step {
+    Codes<BITS> c[4];
+    unsigned short s[4];
+};
 }  // namespace
 
 template <int BITS, int PHASE, int MAXN>
 __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(TcArgs p) {
     using C = Cfg<BITS, PHASE, MAXN>;
-    constexpr int SA = C::SA, SB = C::SB, ACC = C::ACC, NM = C::NM, DEQ = C::DEQ;
-    constexpr int kEpi0 = DEQ, kMma = DEQ + 4, kLoad0 = DEQ + 5;
+    constexpr int SA = C::SA, SB = C::SB, ACC = C::ACC, NM = C::NM, ND = C::ND;
+    constexpr int kEpi0 = C::DEQ, kMma = kEpi0 + C::EPI, kLoad0 = kMma + 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    int32_t *tok_s = reinterpret_cast<int32_t *>(smem + C::OFF_TOK);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *fullA = bars, *emptyA = bars + SA, *fullB = bars + 2 * SA, *emptyB = bars + 2 * SA + SB;
     uint64_t *accF = bars + 2 * SA + 2 * SB, *accE = accF + 2, *drain = accF + 4;
@@ -159,12 +165,12 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
     const FfnBackward &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = a.H, I = a.I;
-    const int MT = PHASE == 1 ? I / kBM : (H + 2 * kBM - 1) / (2 * kBM);
-    const int nk = (PHASE == 1 ? H : 2 * I) / kBK;
+    const int MT = (PHASE == 1 ? I : H) / kBM;                // weight tiles of 128 rows
+    const int nk = (PHASE == 1 ? H : 2 * I) / C::KSTAGE;      // stages of a tile (even)
     if (tid == 0) {
         abort_s = 0;
         for (int i = 0; i < SA; ++i) {
-            mbar_init(fullA + i, DEQ);
+            mbar_init(fullA + i, C::GROUP);
             mbar_init(emptyA + i, 1);
         }
         for (int i = 0; i < SB; ++i) {
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(accF + i, 1);
-            mbar_init(accE + i, 4);
+            mbar_init(accE + i, C::EPI);
         }
         mbar_init(drain, 1);
         fence_barrier_init();
@@ -192,215 +198,162 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
     const int n_my = bid < total ? (total - 1 - bid) / grid + 1 : 0;
     auto tile_of = [&](int i, int &m0) {
         const int t = bid + i * grid, g = t / MT;
-        m0 = (t - g * MT) * (PHASE == 1 ? kBM : 2 * kBM);
+        m0 = (t - g * MT) * kBM;
         return p.tiles[g];
     };
     auto fail = [&]() {
         report(a.err, MOE_DEVERR_TIMEOUT);
         abort_s = 1;
     };
-    auto aborted = [&]() { return __shfl_sync(0xffffffffu, abort_s, 0) != 0; };
-    // one lane polls, the warp follows
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait(bar, parity, p.spin);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) fail();
-        return ok != 0;
+    auto poll = [&](uint64_t *bar, uint32_t parity) {         // one thread's wait, bounded
+        if (mbar_try_wait(bar, parity)) return true;
+        for (long i = 0; i < p.spin; ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (abort_s) return false;
+        }
+        fail();
+        return false;
+    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) {         // a warp's wait: the same answer on every lane
+        return __all_sync(0xffffffffu, poll(bar, parity)) != 0;
     };
 
-    if (warp < DEQ) {
+    if (warp < C::DEQ) {
         // ------------------------------------------------- dequantisation
-        const uint32_t sA = smem_addr(smem);
-        const int b = lane & 3, rl = lane >> 2, w4 = warp & 3;
+        // Group 0 takes the even stages, group 1 the odd ones.
+        const int group = warp / C::GROUP, t = tid - group * 32 * C::GROUP;
         constexpr int BB = 4 * BITS;                          // bytes of a block's codes
-        if constexpr (PHASE == 1) {
-            // matrix g, u or q = warp / 4; steps of 128 K values, two stages each
-            const int mat = warp >> 2, nslot = nk / 2;
-            const bool trans = mat == 2;
-            const bool odd = b >= 2;                          // takes the odd row of a pair
-            struct Slot {
-                Codes<BITS> c[4];
-                uint2 s[2];                                   // steps: two rows of four, or four rows of one
-            } cur, nxt;
-            const int U = n_my * nslot;
-            auto issue = [&](int u, Slot &o) {
-                int m0;
-                const TokTile te = tile_of(u / nslot, m0);
-                const int sl = u % nslot;
-                const BlobView bv = blob_view(te.blob, BITS, H, I);
-                if (!trans) {
-                    const uint8_t *codes = (mat ? bv.cu : bv.cg) + (4 * sl + b) * BB;
-                    const size_t rowb = static_cast<size_t>(H) * BITS / 8;
-                    const __half *sc = (mat ? bv.su : bv.sg) + 4 * sl;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o.c[i] = load_codes<BITS>(codes + (m0 + 32 * w4 + 16 * (i >> 1) + 2 * rl + (i & 1)) * rowb);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        o.s[i] = __ldg(reinterpret_cast<const uint2 *>(
-                            sc + static_cast<size_t>(m0 + 32 * w4 + 16 * i + 2 * rl + odd) * (H / 32)));
-                } else {
-                    const uint8_t *codes = bv.cd + (m0 / 32 + b) * BB;
-                    const size_t rowb = static_cast<size_t>(I) * BITS / 8;
-                    const unsigned short *sc = reinterpret_cast<const unsigned short *>(bv.sd) + m0 / 32 + b;
-                    uint32_t s[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const size_t h = 128 * sl + 32 * i + 8 * w4 + rl;
-                        o.c[i] = load_codes<BITS>(codes + h * rowb);
-                        s[i] = __ldg(sc + h * (I / 32));
-                    }
-                    o.s[0] = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
-                }
-            };
-            if (U) issue(0, cur);
-            for (int u = 0; u < U && !aborted(); ++u) {
-                if (u + 1 < U) issue(u + 1, nxt);
-                if (!trans) {
-                    // lanes 0, 1 of a row's four take the even row of each pair (their own block of the
-                    // first stage, the neighbour's of the second), lanes 2, 3 the odd row
-#pragma unroll
-                    for (int i = 0; i < 4; i += 2)
-#pragma unroll
-                        for (int x = 0; x < BITS; ++x) {
-                            const uint32_t give = odd ? cur.c[i].w[x] : cur.c[i + 1].w[x];
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 2);
-                            if (odd) cur.c[i].w[x] = got;
-                            else cur.c[i + 1].w[x] = got;
-                        }
-                }
-                bool ok = true;
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const int j = 2 * u + ks, sa = j % SA;
-                    ok = ok && wait(emptyA + sa, ((j / SA) & 1) ^ 1);
-                    if (!ok) break;
-                    const uint32_t tile = sA + sa * C::A_STAGE + mat * kMat;
-                    if (!trans) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int row = 32 * w4 + 16 * i + 2 * rl + odd;
-                            put_block<BITS>(cur.c[2 * i + ks], half_of(cur.s[i], 2 * ks + (b & 1)), tile + row * 128,
-                                            4 * (b & 1), row & 7, false);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int k = 32 * i + 8 * w4 + rl;
-                            put_block<BITS>(cur.c[2 * ks + i], half_of(cur.s[0], 2 * ks + i),
-                                            tile + (b >> 1) * 8192 + k * 128, 4 * (b & 1), k & 7, odd);
-                        }
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(fullA + sa);
-                }
-                if (!ok) break;
-                cur = nxt;
+        // phase 1: g and u: (row + 32 i, half of the stage's K); q and phase 2: (K index + KS i, block of
+        // columns).  Neighbouring lanes take the blocks of a row: whole sectors.
+        const int mat = PHASE == 1 ? t >> 6 : 0;
+        const bool trans = PHASE == 2 || mat == 2;
+        constexpr int KS = PHASE == 1 ? 16 : 32;
+        const int tt = PHASE == 1 ? t & 63 : t;
+        const int b = trans ? tt & 3 : tt & 1, r = trans ? tt >> 2 : tt >> 1;
+        // the source of the next stage: pointers of the first block, distances of the others and of stages
+        const uint8_t *cp = nullptr;
+        const unsigned short *sp = nullptr;
+        const int rowb = (PHASE == 1 && trans ? I : H) * BITS / 8, rows = (PHASE == 1 && trans ? I : H) / 32;
+        const int cs = (trans ? KS : 32) * rowb, ss = (trans ? KS : 32) * rows;
+        const int cstep = trans ? 2 * kBK * rowb : 4 * BB, sstep = trans ? 2 * kBK * rows : 4;      // phase 1
+        int st = nk, next = 0, m0 = 0;                        // the next stage, the tile after this one
+        BlobView bv = {};
+        auto fetch = [&](Step<BITS> &o) {
+            const bool start = st >= nk;
+            if (start) {
+                const TokTile te = tile_of(next++, m0);
+                bv = blob_view(te.blob, BITS, H, I);
+                st = group;
             }
-        } else {
-            // 64 rows of Wg, then Wu, a stage: 256 columns, two tiles of 128
-            struct Step {
-                Codes<BITS> c[2];
-                uint32_t s;
-            } ring[2];
-            const int J = n_my * nk;
-            auto issue = [&](int j, Step &o) {
-                int m0;
-                const TokTile te = tile_of(j / nk, m0);
-                const BlobView bv = blob_view(te.blob, BITS, H, I);
-                int i = (j % nk) * kBK + 8 * warp + rl;
-                const bool up = i >= I;
-                if (up) i -= I;
-                const uint8_t *codes = (up ? bv.cu : bv.cg) + i * (static_cast<size_t>(H) * BITS / 8) + (m0 / 32 + b) * BB;
-                const unsigned short *sc = reinterpret_cast<const unsigned short *>(up ? bv.su : bv.sg) +
-                                           static_cast<size_t>(i) * (H / 32) + m0 / 32 + b;
-                const bool two = m0 + kBM < H;
-                o.c[0] = load_codes<BITS>(codes);
-                o.s = __ldg(sc);
-                if (two) {
-                    o.c[1] = load_codes<BITS>(codes + 4 * BB);
-                    o.s |= static_cast<uint32_t>(__ldg(sc + 4)) << 16;
-                } else {
-                    o.c[1] = o.c[0];                          // a ragged last tile: written, not used
-                }
-            };
-            if (J > 0) issue(0, ring[0]);
-            if (J > 1) issue(1, ring[1]);
-            for (int j = 0; j < J && !aborted(); ++j) {
-                const Step cur = ring[0];
-                ring[0] = ring[1];
-                if (j + 2 < J) issue(j + 2, ring[1]);
-                const int sa = j % SA;
-                if (!wait(emptyA + sa, ((j / SA) & 1) ^ 1)) break;
-                const uint32_t row = sA + sa * C::A_STAGE + (b >> 1) * 8192 + (8 * warp + rl) * 128;
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    put_block<BITS>(cur.c[m], half_of(make_uint2(cur.s, 0), m), row + m * kMat, 4 * (b & 1), rl, b >= 2);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(fullA + sa);
+            if (PHASE == 2 || start) {
+                // phase 2: Wg's I / 128 stages, then Wu's
+                const bool up = PHASE == 2 && st * C::KSTAGE >= I;
+                const uint8_t *codes = PHASE == 2 ? (up ? bv.cu : bv.cg) : mat == 0 ? bv.cg : mat == 1 ? bv.cu : bv.cd;
+                const __half *steps = PHASE == 2 ? (up ? bv.su : bv.sg) : mat == 0 ? bv.sg : mat == 1 ? bv.su : bv.sd;
+                const size_t row = trans ? st * C::KSTAGE - (up ? I : 0) + r : m0 + r;
+                const int col = trans ? m0 / 32 + b : 2 * group + b;
+                cp = codes + row * rowb + col * BB;
+                sp = reinterpret_cast<const unsigned short *>(steps) + row * rows + col;
             }
+            st += 2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o.c[i] = load_codes<BITS>(cp + static_cast<size_t>(i) * cs);
+                o.s[i] = __ldg(sp + static_cast<size_t>(i) * ss);
+            }
+            if (PHASE == 1) cp += cstep, sp += sstep;
+        };
+        // where the thread's blocks go within a stage
+        const uint32_t sA = smem_addr(smem);
+        const uint32_t to = trans ? mat * kMat + (b >> 1) * 8192 + r * 128 : mat * kMat + r * 128;
+        const int c0 = trans ? 4 * (b & 1) : 4 * b, sw = r & 7;
+        const bool flip = trans && b >= 2;
+        int sa = group % SA;
+        uint32_t phase = 1;                                   // the first pass over the ring finds it empty
+        auto put = [&](const Step<BITS> &o) {
+            if (!wait(emptyA + sa, phase)) return false;
+            const uint32_t at = sA + sa * C::A_STAGE + to;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // rows 32 i on (32 x 128 bytes); K rows KS i on: 128 bytes each, 64 rows a tile
+                const uint32_t off = PHASE == 1 ? (trans ? i * KS * 128 : i * 32 * 128)
+                                                : (i >> 1) * kMat + (i & 1) * KS * 128;
+                put_block<BITS>(o.c[i], __ushort_as_half(o.s[i]), at + off, c0, sw, flip);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fullA + sa);
+            sa += 2;
+            if (sa >= SA) sa -= SA, phase ^= 1;
+            return true;
+        };
+        Step<BITS> s0, s1;
+        const int n = n_my * (nk / 2);
+        if (n > 0) fetch(s0);
+        if (n > 1) fetch(s1);
+        for (int i = 0; i < n; i += 2) {
+            if (!put(s0)) break;
+            if (i + 2 < n) fetch(s0);
+            if (i + 1 >= n || !put(s1)) break;
+            if (i + 3 < n) fetch(s1);
         }
     } else if (warp >= kLoad0) {
         // --------------------------------------------------- rows of x, dy or [dg | du]
-        const int lw = warp - kLoad0, c = lane & 7;
-        constexpr int ROWS = MAXN / C::LOAD;
-        int32_t *tok = tok_s + lw * ROWS;
-        const size_t rowb = static_cast<size_t>(PHASE == 1 ? H : 2 * I) * 2;
-        const uint8_t *src0 = reinterpret_cast<const uint8_t *>(PHASE == 1 ? p.x16 : p.gu16) + c * 16;
-        const uint8_t *src1 = reinterpret_cast<const uint8_t *>(p.dy16) + c * 16;
-        const int J = n_my * nk;
-        constexpr int D = 1;                                  // steps of copies in flight beyond the one issued
-        int cur = -1, N = 0, n = 0;
-        for (int j = 0; j < J + D; ++j) {
-            if (aborted()) break;
-            if (j < J) {
-                const int i = j / nk, s = j - i * nk;
-                if (i != cur) {
-                    int m0;
-                    const TokTile te = tile_of(i, m0);
-                    cur = i;
-                    n = te.n;
-                    N = (n + 15) & ~15;
-                    __syncwarp();
-                    for (int r = lane; r < ROWS; r += 32) {
-                        const int q = lw * ROWS + r;
-                        int v = 0;
-                        if (q < n) {
-                            if (PHASE == 2) v = (te.row0 >= 0 ? te.row0 : a.T * a.k) + te.n0 + q;
-                            else v = te.row0 >= 0
-                                         ? guard_index(a.perm_src[te.row0 + te.n0 + q], a.T, a.err, MOE_DEVERR_BAD_ROW)
-                                         : te.n0 + q;
-                        }
-                        tok[r] = v;
-                    }
-                    __syncwarp();
+        const int lw = warp - kLoad0, c = lane & 7, r0 = lw * (MAXN / C::LOAD) + (lane >> 3);
+        constexpr int R = MAXN / C::LOAD / 4;                 // rows of a lane: r0 + 4 r
+        const uint32_t row16 = (PHASE == 1 ? H : 2 * I) / 8;  // 16-byte pieces of a row
+        const uint4 *src0 = reinterpret_cast<const uint4 *>(PHASE == 1 ? p.x16 : p.gu16) + c;
+        const uint4 *src1 = PHASE == 1 ? reinterpret_cast<const uint4 *>(p.dy16) + c : src0 + 8;
+        constexpr int D = 1;                                  // stages of copies in flight beyond the one issued
+        int sb = 0, pub = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        auto publish = [&]() {                                // the stage issued D stages ago has landed
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fullB + pub);
+            if (++pub == SB) pub = 0;
+        };
+        int issued = 0;
+        for (int i = 0; i < n_my && ok; ++i) {
+            int m0;
+            const TokTile te = tile_of(i, m0);
+            const int N = (te.n + 15) & ~15;
+            size_t off[R];                                    // pieces from src0 to the row's start
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int q = r0 + 4 * r;
+                int v = 0;
+                if (q < te.n) {
+                    if (PHASE == 2) v = (te.row0 >= 0 ? te.row0 : a.T * a.k) + te.n0 + q;
+                    else v = te.row0 >= 0 ? guard_index(a.perm_src[te.row0 + te.n0 + q], a.T, a.err, MOE_DEVERR_BAD_ROW)
+                                          : te.n0 + q;
                 }
-                const int sb = j % SB;
-                if (!wait(emptyB + sb, ((j / SB) & 1) ^ 1)) break;
-                const uint32_t dst = smem_addr(smem + C::OFF_B + sb * C::B_STAGE);
-#pragma unroll 4
-                for (int r = lane >> 3; r < ROWS; r += 4) {
-                    const int q = lw * ROWS + r;
-                    if (q < N) {
-                        const size_t off = static_cast<size_t>(tok[r]) * rowb + static_cast<size_t>(s) * 128;
-                        const uint32_t to = dst + q * 128 + ((c ^ (q & 7)) << 4), bytes = q < n ? 16u : 0u;
-                        cp_async16(to, src0 + off, bytes);
-                        if (PHASE == 1) cp_async16(to + C::B_TILE, src1 + off, bytes);
-                    }
-                }
+                off[r] = static_cast<size_t>(v) * row16;
             }
-            cp_async_commit();
-            if (j >= D) {
-                cp_async_wait<D>();
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(fullB + (j - D) % SB);
+            for (int s = 0; s < nk; ++s) {
+                if (!(ok = wait(emptyB + sb, phase))) break;
+                const uint32_t dst = smem_addr(smem + C::OFF_B + sb * C::B_STAGE) + r0 * 128;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int q = r0 + 4 * r;
+                    if (q < N) {
+                        const uint32_t to = dst + r * 512 + ((c ^ (q & 7)) << 4), bytes = q < te.n ? 16u : 0u;
+                        const size_t at = off[r] + static_cast<uint32_t>(s * (C::KSTAGE / 8));
+                        cp_async16(to, src0 + at, bytes);
+                        cp_async16(to + C::B_TILE, src1 + at, bytes);
+                    }
+                }
+                if (++sb == SB) sb = 0, phase ^= 1;
+                cp_async_commit();
+                if (issued++ >= D) {
+                    cp_async_wait<D>();
+                    publish();
+                }
             }
         }
         cp_async_wait<0>();
+        for (int i = 0; i < D && i < issued && ok; ++i) publish();
     } else if (warp < kMma) {
         // -------------------------------------------------------- epilogue
         const int q = warp - kEpi0;                           // TMEM lanes 32q .. 32q + 31
@@ -410,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
         // each warp has its own table of the tile's scales: no barrier among
         // the four, of which one may leave early
         float *sx_s = reinterpret_cast<float *>(smem + C::OFF_SX) + q * MAXN;
-        for (int i = 0; i < n_my && !aborted(); ++i) {
+        for (int i = 0; i < n_my; ++i) {
             int m0;
             const TokTile te = tile_of(i, m0);
             const size_t row0 = static_cast<size_t>(te.row0 >= 0 ? te.row0 : a.T * a.k) + te.n0;
@@ -426,7 +379,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
             const int acc = i % ACC;
             if (!wait(accF + acc, (i / ACC) & 1)) break;
             tc_fence_after();
-            const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * NM * MAXN;
+            const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * ND * MAXN;
             if constexpr (PHASE == 1) {
                 for (int c0 = 0; c0 < te.n; c0 += 16) {
                     float gv[16], uv[16], qv[16];
@@ -463,18 +416,14 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
                     if (!(lane & 1) && te.row0 >= 0 && r < te.n) p.dwp[(row0 + r) * (I / 32) + m0 / 32 + q] = sum;
                 }
             } else {
-                for (int mat = 0; mat < 2; ++mat) {
-                    const int h = m0 + kBM * mat + m;
-                    if (m0 + kBM * mat >= H) break;
-                    for (int c0 = 0; c0 < te.n; c0 += 16) {
-                        float v[16];
-                        tmem_ld16(base + mat * MAXN + c0, v);
-                        tmem_ld_wait();
-                        float *out = p.dxp + (row0 + c0) * H + h;
+                for (int c0 = 0; c0 < te.n; c0 += 16) {
+                    float v[16];
+                    tmem_ld16(base + c0, v);
+                    tmem_ld_wait();
+                    float *out = p.dxp + (row0 + c0) * H + m0 + m;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c0 + e < te.n) out[static_cast<size_t>(e) * H] = v[e];
-                    }
+                    for (int e = 0; e < 16; ++e)
+                        if (c0 + e < te.n) out[static_cast<size_t>(e) * H] = v[e];
                 }
             }
             tc_fence_before();
@@ -483,43 +432,43 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
         }
     } else {
         // ------------------------------------------------------ MMA issuer
-        for (int i = 0; i < n_my && !aborted(); ++i) {
-            int m0;
-            const TokTile te = tile_of(i, m0);
-            const int N = (te.n + 15) & ~15, acc = i % ACC;
-            const int nmat = PHASE == 1 || m0 + kBM < H ? NM : 1;
-            const uint32_t id_k = idesc_16bit(0, 0, 0, kBM, N), id_mn = idesc_16bit(0, 1, 0, kBM, N);
-            if (lane == 0) {
-                if (!mbar_wait(accE + acc, ((i / ACC) & 1) ^ 1, p.spin)) fail();
+        if (lane == 0) {
+            const uint64_t mn = desc_mn_sw128(smem_addr(smem), 8192, 1024), km = desc_sw128(smem_addr(smem));
+            int sa = 0, sb = 0;
+            uint32_t pa = 0, pb = 0;
+            bool ok = true;
+            for (int i = 0; i < n_my && ok; ++i) {
+                int m0;
+                const TokTile te = tile_of(i, m0);
+                const int N = (te.n + 15) & ~15, acc = i % ACC;
+                const uint32_t id_k = idesc_16bit(0, 0, 0, kBM, N), id_mn = idesc_16bit(0, 1, 0, kBM, N);
+                const uint32_t d = tmem + acc * ND * MAXN;
+                if (!(ok = poll(accE + acc, ((i / ACC) & 1) ^ 1))) break;
                 tc_fence_after();
-                for (int s = 0; s < nk && !abort_s; ++s) {
-                    const int j = i * nk + s, sa = j % SA, sb = j % SB;
-                    if (!mbar_spin(fullB + sb, (j / SB) & 1, p.spin * 16) ||
-                        !mbar_spin(fullA + sa, (j / SA) & 1, p.spin * 16)) {
-                        fail();
-                        break;
-                    }
+                for (int s = 0; s < nk; ++s) {
+                    if (!(ok = poll(fullB + sb, pb) && poll(fullA + sa, pa))) break;
                     tc_fence_after();
-                    const uint32_t bs = smem_addr(smem + C::OFF_B + sb * C::B_STAGE);
-                    const uint32_t as = smem_addr(smem + sa * C::A_STAGE);
+                    // descriptors count in 16 bytes from the ring's start
+                    const uint64_t as = (sa * C::A_STAGE) >> 4, bs = (C::OFF_B + sb * C::B_STAGE) >> 4;
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk) {
-                        for (int mat = 0; mat < nmat; ++mat) {
-                            const bool mn = PHASE == 2 || mat == 2;
-                            const uint32_t at = as + mat * kMat;
-                            mma_f16(tmem + (acc * NM + mat) * MAXN,
-                                    mn ? desc_mn_sw128(at + kk * 2048, 8192, 1024) : desc_sw128(at + kk * 32),
-                                    desc_sw128(bs + (PHASE == 1 && mat == 2 ? C::B_TILE : 0) + kk * 32),
-                                    mn ? id_mn : id_k, (s | kk) != 0);
-                        }
+                    for (int mat = 0; mat < NM; ++mat) {
+                        const bool trans = PHASE == 2 || mat == 2;
+                        const uint64_t am = as + mat * (kMat >> 4);
+                        const uint64_t bm = bs + (PHASE == 1 ? mat == 2 : mat) * (C::B_TILE >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            mma_f16(d + (PHASE == 1 ? mat : 0) * MAXN, trans ? mn + am + kk * 128 : km + am + kk * 2,
+                                    km + bm + kk * 2, trans ? id_mn : id_k, (PHASE == 1 ? s | kk : s | kk | mat) != 0);
                     }
                     mma_commit(emptyA + sa);
                     mma_commit(emptyB + sb);
+                    if (++sa == SA) sa = 0, pa ^= 1;
+                    if (++sb == SB) sb = 0, pb ^= 1;
                 }
                 mma_commit(accF + acc);
             }
-            __syncwarp();
         }
+        __syncwarp();
         if (lane == 0) {                                      // TMEM is released once every MMA is done
             mma_commit(drain);
             if (!mbar_wait(drain, 0, kSpin)) report(a.err, MOE_DEVERR_TIMEOUT);
@@ -728,8 +677,8 @@ size_t ffn_backward_gemm_ws_bytes(int T, int k, int H, int I, int E) { return ca
 bool ffn_backward_gemm_supported(int T, int k, int H, int I, int E) {
     // tile and step numbers are ints
     const TcPlan p = plan_of(T, k, E);
-    const double n1 = static_cast<double>(p.tiles1) * (I / kBM), n2 = static_cast<double>(p.tiles2) * ((H + 255) / 256);
-    return n1 < 2e9 && n2 < 2e9 && n1 / num_sms() * (H / kBK) < 2e9 && n2 / num_sms() * (2 * I / kBK) < 2e9;
+    const double n1 = static_cast<double>(p.tiles1) * (I / kBM), n2 = static_cast<double>(p.tiles2) * (H / kBM);
+    return n1 < 2e9 && n2 < 2e9 && (n1 / num_sms() + 1) * (H / kBK) < 2e9 && (n2 / num_sms() + 1) * (I / kBK) < 2e9;
 }
 
 int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
