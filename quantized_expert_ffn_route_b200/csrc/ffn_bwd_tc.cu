@@ -16,19 +16,25 @@
 // activation, and dg, du are kept in the scaled form,
 //   dg / (sx sd) = q' u' (s + a (1 - s)),   du / (sx sd) = q' a',
 // until the gather multiplies by w sx sd in fp32.
+// They lie transposed between the phases, [2I] x rows, a group's rows padded
+// to 16: a thread of phase 1 holds one i and 16 rows, 32 bytes to store, and
+// phase 2 takes its N side MN-major as it takes the weights.
 //
 // One persistent block per SM.  Roles:
 //   dequantising warps, two groups that take alternate stages, read codes
 //       straight to registers two of their stages ahead (no shared memory is
 //       spent on codes) and write fp16 tiles to the A stages, four blocks of 32
 //       a thread between two barriers;
-//   loader warps gather the rows (cp.async) into the B stages;
+//   loader warps fill the B stages: phase 1 gathers the tokens' rows with
+//       cp.async (TMA's four-row gathers took 50 cycles each here: 1842 us at
+//       8192 tokens), phase 2 one warp with TMA boxes of 64 K rows x 64 tokens;
 //   one thread issues tcgen05.mma; four warps read the accumulators.
 // Every wait is bounded (MOE_DEVERR_TIMEOUT; all roles then leave their loops
 // and TMEM is freed).
 #include "common.cuh"
 #include "kernels.h"
 #include "train/ffn_bwd.cuh"
+#include "train/tma.cuh"
 #include "train/umma.cuh"
 
 namespace moe {
@@ -46,14 +52,16 @@ struct __align__(16) TokTile {
     const uint8_t *blob;
     int row0;      // first permuted row of the group, or -1 for the shared expert
     int n0, n;
-    int pad[3];
+    int at;        // column of gu16 of the first row
+    int pad[2];
 };
 
 struct TcArgs {
     FfnBackward a;
-    const __half *x16, *dy16;     // [T, H], scaled
     const float2 *scale;          // [T]: sx, sd
-    __half *gu16;                 // [T*k + T, 2I]: dg, du, scaled
+    __half *gu16;                 // [2I, cols]: dg, du, scaled, a column per row of a group
+    int cols;
+    const __half *x16, *dy16;     // [T, H], scaled
     float *dwp;                   // [T*k, I/32]
     float *dxp;                   // [T*k + T, H]
     uint8_t *ok;                  // [T*k]
@@ -76,7 +84,7 @@ struct Cfg {
     static constexpr int GROUP = PHASE == 1 ? 6 : 4;          // warps of a dequantising group: 4 blocks a thread
     static constexpr int DEQ = 2 * GROUP;
     static constexpr int EPI = 4;
-    static constexpr int LOAD = 4;                            // loader warps
+    static constexpr int LOAD = PHASE == 1 ? 7 : 1;           // loader warps
     static constexpr int THREADS = 32 * (DEQ + EPI + 1 + LOAD);
     static constexpr uint32_t A_STAGE = NM * kMat;
     static constexpr uint32_t B_TILE = MAXN * 128;
@@ -92,7 +100,7 @@ struct Cfg {
     static_assert(SMEM <= kSmemMax, "shared memory per block");
     static_assert(2 * SA + 2 * SB + 5 <= 24, "barrier slots");
     static_assert(ACC * ND * MAXN <= 512, "TMEM columns");
-    static_assert(MAXN % (4 * LOAD) == 0 && MAXN % 16 == 0 && MAXN <= 256, "rows per loader warp");
+    static_assert(MAXN % 16 == 0 && MAXN <= 256 && (PHASE == 1 || MAXN % 64 == 0), "tokens a tile");
 };
 
 // One block's codes as read: four words (4 bits) or two.
@@ -151,7 +159,8 @@ template <int BITS> struct Step {
 }  // namespace
 
 template <int BITS, int PHASE, int MAXN>
-__global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(TcArgs p) {
+__global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
+    TcArgs p, const __grid_constant__ CUtensorMap map) {
     using C = Cfg<BITS, PHASE, MAXN>;
     constexpr int SA = C::SA, SB = C::SB, ACC = C::ACC, NM = C::NM, ND = C::ND;
     constexpr int kEpi0 = C::DEQ, kMma = kEpi0 + C::EPI, kLoad0 = kMma + 1;
@@ -174,7 +183,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
             mbar_init(emptyA + i, 1);
         }
         for (int i = 0; i < SB; ++i) {
-            mbar_init(fullB + i, C::LOAD);
+            mbar_init(fullB + i, PHASE == 1 ? C::LOAD : 1);   // phase 2: and the copies' bytes
             mbar_init(emptyB + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -297,15 +306,13 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
             if (i + 1 >= n || !put(s1)) break;
             if (i + 3 < n) fetch(s1);
         }
-    } else if (warp >= kLoad0) {
-        // --------------------------------------------------- rows of x, dy or [dg | du]
-        const int lw = warp - kLoad0, c = lane & 7, r0 = lw * (MAXN / C::LOAD) + (lane >> 3);
-        constexpr int R = MAXN / C::LOAD / 4;                 // rows of a lane: r0 + 4 r
-        const uint32_t row16 = (PHASE == 1 ? H : 2 * I) / 8;  // 16-byte pieces of a row
-        const uint4 *src0 = reinterpret_cast<const uint4 *>(PHASE == 1 ? p.x16 : p.gu16) + c;
-        const uint4 *src1 = PHASE == 1 ? reinterpret_cast<const uint4 *>(p.dy16) + c : src0 + 8;
+    } else if (PHASE == 1 && warp >= kLoad0) {
+        // ------------------------------------------------- rows of x and dy
+        // A warp instruction copies 128 bytes of four rows.
+        const int lw = warp - kLoad0, c = lane & 7, r0 = 4 * lw + (lane >> 3);
+        constexpr int RSTEP = 4 * C::LOAD, R = (MAXN + RSTEP - 1) / RSTEP;     // rows of a lane: r0 + RSTEP r
         constexpr int D = 1;                                  // stages of copies in flight beyond the one issued
-        int sb = 0, pub = 0;
+        int sb = 0, pub = 0, issued = 0;
         uint32_t phase = 1;
         bool ok = true;
         auto publish = [&]() {                                // the stage issued D stages ago has landed
@@ -314,34 +321,31 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
             if (lane == 0) mbar_arrive(fullB + pub);
             if (++pub == SB) pub = 0;
         };
-        int issued = 0;
         for (int i = 0; i < n_my && ok; ++i) {
             int m0;
             const TokTile te = tile_of(i, m0);
             const int N = (te.n + 15) & ~15;
-            size_t off[R];                                    // pieces from src0 to the row's start
+            size_t off[R];                                    // values from x16's (dy16's) start to the row's
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int q = r0 + 4 * r;
+                const int q = r0 + RSTEP * r;
                 int v = 0;
-                if (q < te.n) {
-                    if (PHASE == 2) v = (te.row0 >= 0 ? te.row0 : a.T * a.k) + te.n0 + q;
-                    else v = te.row0 >= 0 ? guard_index(a.perm_src[te.row0 + te.n0 + q], a.T, a.err, MOE_DEVERR_BAD_ROW)
-                                          : te.n0 + q;
-                }
-                off[r] = static_cast<size_t>(v) * row16;
+                if (q < te.n)
+                    v = te.row0 >= 0 ? guard_index(a.perm_src[te.row0 + te.n0 + q], a.T, a.err, MOE_DEVERR_BAD_ROW)
+                                     : te.n0 + q;
+                off[r] = static_cast<size_t>(v) * H + 8 * c;
             }
             for (int s = 0; s < nk; ++s) {
                 if (!(ok = wait(emptyB + sb, phase))) break;
-                const uint32_t dst = smem_addr(smem + C::OFF_B + sb * C::B_STAGE) + r0 * 128;
+                const uint32_t dst = smem_addr(smem + C::OFF_B + sb * C::B_STAGE);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const int q = r0 + 4 * r;
+                    const int q = r0 + RSTEP * r;
                     if (q < N) {
-                        const uint32_t to = dst + r * 512 + ((c ^ (q & 7)) << 4), bytes = q < te.n ? 16u : 0u;
-                        const size_t at = off[r] + static_cast<uint32_t>(s * (C::KSTAGE / 8));
-                        cp_async16(to, src0 + at, bytes);
-                        cp_async16(to + C::B_TILE, src1 + at, bytes);
+                        const uint32_t to = dst + q * 128 + ((c ^ (q & 7)) << 4), bytes = q < te.n ? 16u : 0u;
+                        const size_t at = off[r] + static_cast<uint32_t>(s * kBK);
+                        cp_async16(to, p.x16 + at, bytes);
+                        cp_async16(to + C::B_TILE, p.dy16 + at, bytes);
                     }
                 }
                 if (++sb == SB) sb = 0, phase ^= 1;
@@ -354,25 +358,53 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
         }
         cp_async_wait<0>();
         for (int i = 0; i < D && i < issued && ok; ++i) publish();
+    } else if (PHASE == 2 && warp >= kLoad0) {
+        // ------------------------------------------------- [dg | du] by TMA
+        int sb = 0, issued = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        if (lane == 0) tma_prefetch_map(&map);
+        for (int i = 0; i < n_my && ok; ++i) {
+            int m0;
+            const TokTile te = tile_of(i, m0);
+            const int half = lane & 1, n0 = (lane >> 1) * 64, boxes = (te.n + 63) / 64;
+            for (int s = 0; s < nk; ++s) {
+                if (!(ok = wait(emptyB + sb, phase))) break;
+                const uint32_t dst = smem_addr(smem + C::OFF_B + sb * C::B_STAGE);
+                if (lane == 0) mbar_arrive_expect_tx(fullB + sb, 2 * boxes * 8192);
+                __syncwarp();
+                if (n0 < te.n)
+                    tma_load_2d(dst + half * C::B_TILE + n0 * 128, &map, te.at + n0, (2 * s + half) * kBK, fullB + sb);
+                if (++sb == SB) sb = 0, phase ^= 1;
+                ++issued;
+            }
+        }
+        // no copy is in flight when the block leaves, also when another role gave up
+        for (int f = max(0, issued - SB); f < issued; ++f)
+            for (long x = 0; x < kSpin && !mbar_try_wait(fullB + f % SB, (f / SB) & 1); ++x) {}
+        __syncwarp();
     } else if (warp < kMma) {
         // -------------------------------------------------------- epilogue
-        const int q = warp - kEpi0;                           // TMEM lanes 32q .. 32q + 31
-        // a warp reads the lanes of its rank modulo four
         static_assert(kEpi0 % 4 == 0, "TMEM lanes follow the warp's rank");
+        const int ew = warp - kEpi0, q = ew & 3;              // TMEM lanes 32q .. 32q + 31
         const int m = 32 * q + lane;
         // each warp has its own table of the tile's scales: no barrier among
-        // the four, of which one may leave early
-        float *sx_s = reinterpret_cast<float *>(smem + C::OFF_SX) + q * MAXN;
+        // them, of which one may leave early
+        float *sx_s = reinterpret_cast<float *>(smem + C::OFF_SX) + ew * MAXN;
         for (int i = 0; i < n_my; ++i) {
             int m0;
             const TokTile te = tile_of(i, m0);
             const size_t row0 = static_cast<size_t>(te.row0 >= 0 ? te.row0 : a.T * a.k) + te.n0;
             if constexpr (PHASE == 1) {
                 __syncwarp();                                 // the last tile's scales are read
-                for (int r = lane; r < te.n; r += 32) {
-                    const int t = te.row0 >= 0 ? guard_index(a.perm_src[te.row0 + te.n0 + r], a.T, nullptr, 0) : te.n0 + r;
-                    sx_s[r] = p.scale[t].x;
-                    if (te.row0 >= 0 && m0 == 0 && q == 0) p.ok[row0 + r] = 1;
+                for (int r = lane; r < ((te.n + 15) & ~15); r += 32) {
+                    float sx = 0.f;
+                    if (r < te.n) {
+                        const int t = te.row0 >= 0 ? guard_index(a.perm_src[te.row0 + te.n0 + r], a.T, nullptr, 0) : te.n0 + r;
+                        sx = p.scale[t].x;
+                        if (te.row0 >= 0 && m0 == 0 && ew == 0) p.ok[row0 + r] = 1;
+                    }
+                    sx_s[r] = sx;
                 }
                 __syncwarp();
             }
@@ -381,39 +413,52 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
             tc_fence_after();
             const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * ND * MAXN;
             if constexpr (PHASE == 1) {
-                for (int c0 = 0; c0 < te.n; c0 += 16) {
+                for (int c0 = 16 * (ew >> 2); c0 < te.n; c0 += 4 * C::EPI) {
                     float gv[16], uv[16], qv[16];
                     tmem_ld16(base + c0, gv);
                     tmem_ld16(base + MAXN + c0, uv);
                     tmem_ld16(base + 2 * MAXN + c0, qv);
                     tmem_ld_wait();
-                    __half *out = p.gu16 + (row0 + c0) * 2 * I + m0 + m;
+                    uint32_t dg[8], du[8];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const bool in = c0 + e < te.n;
-                        const float g = gv[e] * (in ? sx_s[c0 + e] : 0.f);
-                        const float s = __fdividef(1.f, 1.f + __expf(-g));
-                        const float qu = qv[e] * uv[e], act = gv[e] * s;       // a / sx
-                        if (in) {
-                            out[static_cast<size_t>(e) * 2 * I] = __float2half_rn(qu * fmaf(g * s, 1.f - s, s));
-                            out[static_cast<size_t>(e) * 2 * I + I] = __float2half_rn(qv[e] * act);
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 sx = *reinterpret_cast<const float2 *>(sx_s + c0 + e);
+                        float vg[2], vu[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float g = gv[e + x] * (x ? sx.y : sx.x);
+                            const float s = __fdividef(1.f, 1.f + __expf(-g));
+                            const float qu = qv[e + x] * uv[e + x], act = gv[e + x] * s;        // a / sx
+                            vg[x] = qu * fmaf(g * s, 1.f - s, s);
+                            vu[x] = qv[e + x] * act;
+                            qv[e + x] = qu * act;
                         }
-                        qv[e] = in ? qu * act : 0.f;
+                        const __half2 hg = __floats2half2_rn(vg[0], vg[1]), hu = __floats2half2_rn(vu[0], vu[1]);
+                        dg[e / 2] = *reinterpret_cast<const uint32_t *>(&hg);
+                        du[e / 2] = *reinterpret_cast<const uint32_t *>(&hu);
                     }
-                    // sixteen rows' sums over the warp's 32 lanes: halves are exchanged, so that each
-                    // step halves the values a lane holds
+                    uint4 *og = reinterpret_cast<uint4 *>(p.gu16 + static_cast<size_t>(m0 + m) * p.cols + te.at + c0);
+                    uint4 *ou = reinterpret_cast<uint4 *>(p.gu16 + static_cast<size_t>(I + m0 + m) * p.cols + te.at + c0);
+                    og[0] = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+                    og[1] = make_uint4(dg[4], dg[5], dg[6], dg[7]);
+                    ou[0] = make_uint4(du[0], du[1], du[2], du[3]);
+                    ou[1] = make_uint4(du[4], du[5], du[6], du[7]);
+                    if (te.row0 >= 0) {
+                        // sixteen rows' sums over the warp's 32 lanes: halves are exchanged, so that each
+                        // step halves the values a lane holds
 #pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) {
-                        const bool up = lane & (2 * o);
+                        for (int o = 8; o > 0; o >>= 1) {
+                            const bool up = lane & (2 * o);
 #pragma unroll
-                        for (int e = 0; e < o; ++e) {
-                            const float give = up ? qv[e] : qv[e + o], keep = up ? qv[e + o] : qv[e];
-                            qv[e] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * o);
+                            for (int e = 0; e < o; ++e) {
+                                const float give = up ? qv[e] : qv[e + o], keep = up ? qv[e + o] : qv[e];
+                                qv[e] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * o);
+                            }
                         }
+                        const float sum = qv[0] + __shfl_xor_sync(0xffffffffu, qv[0], 1);
+                        const int r = c0 + (lane >> 1);
+                        if (!(lane & 1) && r < te.n) p.dwp[(row0 + r) * (I / 32) + m0 / 32 + q] = sum;
                     }
-                    const float sum = qv[0] + __shfl_xor_sync(0xffffffffu, qv[0], 1);
-                    const int r = c0 + (lane >> 1);
-                    if (!(lane & 1) && te.row0 >= 0 && r < te.n) p.dwp[(row0 + r) * (I / 32) + m0 / 32 + q] = sum;
                 }
             } else {
                 for (int c0 = 0; c0 < te.n; c0 += 16) {
@@ -421,9 +466,14 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
                     tmem_ld16(base + c0, v);
                     tmem_ld_wait();
                     float *out = p.dxp + (row0 + c0) * H + m0 + m;
+                    if (c0 + 16 <= te.n) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (c0 + e < te.n) out[static_cast<size_t>(e) * H] = v[e];
+                        for (int e = 0; e < 16; ++e) out[static_cast<size_t>(e) * H] = v[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (c0 + e < te.n) out[static_cast<size_t>(e) * H] = v[e];
+                    }
                 }
             }
             tc_fence_before();
@@ -432,47 +482,46 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(T
         }
     } else {
         // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint64_t mn = desc_mn_sw128(smem_addr(smem), 8192, 1024), km = desc_sw128(smem_addr(smem));
-            int sa = 0, sb = 0;
-            uint32_t pa = 0, pb = 0;
-            bool ok = true;
-            for (int i = 0; i < n_my && ok; ++i) {
-                int m0;
-                const TokTile te = tile_of(i, m0);
-                const int N = (te.n + 15) & ~15, acc = i % ACC;
-                const uint32_t id_k = idesc_16bit(0, 0, 0, kBM, N), id_mn = idesc_16bit(0, 1, 0, kBM, N);
-                const uint32_t d = tmem + acc * ND * MAXN;
-                if (!(ok = poll(accE + acc, ((i / ACC) & 1) ^ 1))) break;
+        const uint32_t on = elect_one();
+        const uint32_t ring = smem_addr(smem), tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t mn = desc_mn_sw128(ring, 8192, 1024), km = desc_sw128(ring);
+        int sa = 0, sb = 0;
+        uint32_t pa = 0, pb = 0;
+        bool ok = true;
+        for (int i = 0; i < n_my && ok; ++i) {
+            int m0;
+            const TokTile te = tile_of(i, m0);
+            const int N = __shfl_sync(0xffffffffu, (te.n + 15) & ~15, 0), acc = i % ACC;
+            const uint32_t id_k = idesc_16bit(0, 0, 0, kBM, N), id_mn = idesc_16bit(0, 1, PHASE == 2, kBM, N);
+            const uint32_t d = tm + acc * ND * MAXN;
+            if (!(ok = wait(accE + acc, ((i / ACC) & 1) ^ 1))) break;
+            tc_fence_after();
+            for (int s = 0; s < nk; ++s) {
+                if (!(ok = wait(fullB + sb, pb)) || !(ok = wait(fullA + sa, pa))) break;
                 tc_fence_after();
-                for (int s = 0; s < nk; ++s) {
-                    if (!(ok = poll(fullB + sb, pb) && poll(fullA + sa, pa))) break;
-                    tc_fence_after();
-                    // descriptors count in 16 bytes from the ring's start
-                    const uint64_t as = (sa * C::A_STAGE) >> 4, bs = (C::OFF_B + sb * C::B_STAGE) >> 4;
+                // descriptors count in 16 bytes from the ring's start
+                const uint64_t as = (sa * C::A_STAGE) >> 4, bs = (C::OFF_B + sb * C::B_STAGE) >> 4;
 #pragma unroll
-                    for (int mat = 0; mat < NM; ++mat) {
-                        const bool trans = PHASE == 2 || mat == 2;
-                        const uint64_t am = as + mat * (kMat >> 4);
-                        const uint64_t bm = bs + (PHASE == 1 ? mat == 2 : mat) * (C::B_TILE >> 4);
+                for (int mat = 0; mat < NM; ++mat) {
+                    const bool trans = PHASE == 2 || mat == 2;
+                    const uint64_t am = as + mat * (kMat >> 4);
+                    const uint64_t bm = bs + (PHASE == 1 ? mat == 2 : mat) * (C::B_TILE >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk)
-                            mma_f16(d + (PHASE == 1 ? mat : 0) * MAXN, trans ? mn + am + kk * 128 : km + am + kk * 2,
-                                    km + bm + kk * 2, trans ? id_mn : id_k, (PHASE == 1 ? s | kk : s | kk | mat) != 0);
-                    }
-                    mma_commit(emptyA + sa);
-                    mma_commit(emptyB + sb);
-                    if (++sa == SA) sa = 0, pa ^= 1;
-                    if (++sb == SB) sb = 0, pb ^= 1;
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        mma_f16_on(on, d + (PHASE == 1 ? mat : 0) * MAXN, trans ? mn + am + kk * 128 : km + am + kk * 2,
+                                   PHASE == 2 ? mn + bm + kk * 128 : km + bm + kk * 2, trans ? id_mn : id_k, (PHASE == 1 ? s | kk : s | kk | mat) != 0);
                 }
-                mma_commit(accF + acc);
+                mma_commit_on(on, emptyA + sa);
+                mma_commit_on(on, emptyB + sb);
+                if (++sa == SA) sa = 0, pa ^= 1;
+                if (++sb == SB) sb = 0, pb ^= 1;
             }
+            mma_commit_on(on, accF + acc);
         }
-        __syncwarp();
-        if (lane == 0) {                                      // TMEM is released once every MMA is done
-            mma_commit(drain);
-            if (!mbar_wait(drain, 0, kSpin)) report(a.err, MOE_DEVERR_TIMEOUT);
-        }
+        mma_commit_on(on, drain);                             // TMEM is released once every MMA is done
+        bool done = false;
+        for (long i = 0; i < kSpin && !done; ++i) done = mbar_try_wait(drain, 0);
+        if (!done) report(a.err, MOE_DEVERR_TIMEOUT);
         __syncwarp();
     }
     tc_fence_before();
@@ -494,6 +543,7 @@ struct Prep {
     int *counts;                  // token tiles of phase 1 and 2
     int max1, max2;               // tokens per tile
     int cap1, cap2;               // entries of the lists
+    int cols;                     // columns of gu16
 };
 
 // 2^-e and 2^e with e = floor(log2 top) of the row's largest |value| (bits
@@ -517,46 +567,48 @@ __device__ __forceinline__ int tile_rows(int n, int most) {
 // one token's x and dy.
 __global__ void __launch_bounds__(kPrepThreads) k_bwd_prepare(FfnBackward a, Prep p) {
     __shared__ uint32_t part[kPrepThreads / 32];
-    __shared__ int2 sums[kPrepThreads / 32];
+    __shared__ int3 sums[kPrepThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (blockIdx.x == 0) {
         const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), a.err);
         const int ng = n_act + (a.shared ? 1 : 0);
-        int2 done = make_int2(0, 0);
+        int3 done = make_int3(0, 0, 0);                       // tiles of phase 1 and 2, columns of gu16
         for (int g0 = 0; g0 < ng; g0 += kPrepThreads) {
             const int g = g0 + tid;
             BwdGroup G = {nullptr, 0, -1};
             if (g < ng) G = bwd_group(a, g, n_act, true);
-            int2 r = make_int2(16, 16), c = make_int2(0, 0);
+            int2 r = make_int2(16, 16);
+            int3 c = make_int3(0, 0, 0);
             if (G.n > 0) {
                 r = make_int2(tile_rows(G.n, p.max1), tile_rows(G.n, p.max2));
-                c = make_int2((G.n + r.x - 1) / r.x, (G.n + r.y - 1) / r.y);
+                c = make_int3((G.n + r.x - 1) / r.x, (G.n + r.y - 1) / r.y, (G.n + 15) & ~15);
             }
-            int2 in = c;                                      // inclusive sums over the warp, then the block
+            int3 in = c;                                      // inclusive sums over the warp, then the block
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, in.x, o), y = __shfl_up_sync(0xffffffffu, in.y, o);
-                if (lane >= o) in.x += x, in.y += y;
+                const int z = __shfl_up_sync(0xffffffffu, in.z, o);
+                if (lane >= o) in.x += x, in.y += y, in.z += z;
             }
             __syncthreads();
             if (lane == 31) sums[warp] = in;
             __syncthreads();
-            int2 at = make_int2(done.x + in.x - c.x, done.y + in.y - c.y);
+            int3 at = make_int3(done.x + in.x - c.x, done.y + in.y - c.y, done.z + in.z - c.z);
             for (int w = 0; w < kPrepThreads / 32; ++w) {
-                if (w < warp) at.x += sums[w].x, at.y += sums[w].y;
-                done.x += sums[w].x, done.y += sums[w].y;
+                if (w < warp) at.x += sums[w].x, at.y += sums[w].y, at.z += sums[w].z;
+                done.x += sums[w].x, done.y += sums[w].y, done.z += sums[w].z;
             }
             // consistent offsets never reach the lists' ends
-            if (at.x + c.x > p.cap1 || at.y + c.y > p.cap2) {
+            if (at.x + c.x > p.cap1 || at.y + c.y > p.cap2 || at.z + c.z > p.cols) {
                 report(a.err, MOE_DEVERR_BAD_ROW);
-                c = make_int2(0, 0);
+                c = make_int3(0, 0, 0);
             }
             for (int i = 0; i < c.x; ++i)
-                p.tiles1[at.x + i] = {G.blob, G.row0, i * r.x, min(r.x, G.n - i * r.x), {0, 0, 0}};
+                p.tiles1[at.x + i] = {G.blob, G.row0, i * r.x, min(r.x, G.n - i * r.x), at.z + i * r.x, {0, 0}};
             for (int i = 0; i < c.y; ++i)
-                p.tiles2[at.y + i] = {G.blob, G.row0, i * r.y, min(r.y, G.n - i * r.y), {0, 0, 0}};
+                p.tiles2[at.y + i] = {G.blob, G.row0, i * r.y, min(r.y, G.n - i * r.y), at.z + i * r.y, {0, 0}};
         }
-        const bool fits = done.x <= p.cap1 && done.y <= p.cap2;
+        const bool fits = done.x <= p.cap1 && done.y <= p.cap2 && done.z <= p.cols;
         if (tid == 0) p.counts[0] = fits ? done.x : 0, p.counts[1] = fits ? done.y : 0;
         return;
     }
@@ -610,6 +662,7 @@ struct TcPlan {
     bool large;
     int max1, max2;
     size_t tiles1, tiles2;        // bounds on the token tiles
+    size_t cols;                  // and on the rows, each group's padded to 16
 };
 constexpr int kSmallN = 64, kLargeN1 = 160, kLargeN2 = 256;
 
@@ -623,6 +676,7 @@ TcPlan plan_of(int T, int k, int E) {
     auto bound = [&](int most) { return static_cast<size_t>(rows / most + groups + T / most + 1); };
     p.tiles1 = bound(p.max1);
     p.tiles2 = bound(p.max2);
+    p.cols = static_cast<size_t>((rows + T + 15 * (groups + 1) + 63) / 64 * 64);
     return p;
 }
 
@@ -647,7 +701,7 @@ size_t carve(int T, int k, int H, int I, int E, uint8_t *base, TcWs *out) {
     TcWs w;
     w.x16 = reinterpret_cast<__half *>(take(static_cast<size_t>(T) * H * 2));
     w.dy16 = reinterpret_cast<__half *>(take(static_cast<size_t>(T) * H * 2));
-    w.gu16 = reinterpret_cast<__half *>(take(all * 2 * I * 2));
+    w.gu16 = reinterpret_cast<__half *>(take(p.cols * 2 * I * 2));
     w.scale = reinterpret_cast<float2 *>(take(static_cast<size_t>(T) * sizeof(float2)));
     w.dwp = reinterpret_cast<float *>(take(rows * (I / 32) * 4));
     w.dxp = reinterpret_cast<float *>(take(all * H * 4));
@@ -660,13 +714,13 @@ size_t carve(int T, int k, int H, int I, int E, uint8_t *base, TcWs *out) {
 }
 
 template <int BITS, int PHASE, int MAXN>
-int launch_phase(const TcArgs &p, cudaStream_t s) {
+int launch_phase(const TcArgs &p, const CUtensorMap &map, cudaStream_t s) {
     using C = Cfg<BITS, PHASE, MAXN>;
     int rc = cuda_status(cudaFuncSetAttribute(k_bwd_tc<BITS, PHASE, MAXN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               static_cast<int>(C::SMEM)),
                          "backward gemm smem attribute");
     if (rc) return rc;
-    k_bwd_tc<BITS, PHASE, MAXN><<<num_sms(), C::THREADS, C::SMEM, s>>>(p);
+    k_bwd_tc<BITS, PHASE, MAXN><<<num_sms(), C::THREADS, C::SMEM, s>>>(p, map);
     count_launches(1);
     return cuda_status(cudaGetLastError(), "backward gemm launch");
 }
@@ -678,6 +732,7 @@ bool ffn_backward_gemm_supported(int T, int k, int H, int I, int E) {
     // tile and step numbers are ints
     const TcPlan p = plan_of(T, k, E);
     const double n1 = static_cast<double>(p.tiles1) * (I / kBM), n2 = static_cast<double>(p.tiles2) * (H / kBM);
+    if (p.cols > 2000000000u) return false;
     return n1 < 2e9 && n2 < 2e9 && (n1 / num_sms() + 1) * (H / kBK) < 2e9 && (n2 / num_sms() + 1) * (I / kBK) < 2e9;
 }
 
@@ -688,21 +743,25 @@ int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     int rc = cuda_status(cudaMemsetAsync(w.ok, 0, static_cast<size_t>(a.T) * a.k, s), "row flags memset");
     if (rc) return rc;
     const Prep prep = {w.x16, w.dy16, w.scale, w.tiles1, w.tiles2, w.counts, plan.max1, plan.max2,
-                       static_cast<int>(plan.tiles1), static_cast<int>(plan.tiles2)};
+                       static_cast<int>(plan.tiles1), static_cast<int>(plan.tiles2),
+                       static_cast<int>(plan.cols)};
     k_bwd_prepare<<<a.T + 1, kPrepThreads, 0, s>>>(a, prep);
     count_launches(1);
     rc = cuda_status(cudaGetLastError(), "backward prepare launch");
     if (rc) return rc;
     const long hook = static_cast<long>(test_hook_value(MOE_HOOK_GEMM_SPIN));
-    TcArgs p = {a, w.x16, w.dy16, w.scale, w.gu16, w.dwp, w.dxp, w.ok, w.tiles1, w.counts, hook > 0 ? hook : kSpin};
+    TcArgs p = {a, w.scale, w.gu16, static_cast<int>(plan.cols), w.x16, w.dy16, w.dwp, w.dxp, w.ok, w.tiles1, w.counts, hook > 0 ? hook : kSpin};
     TcArgs p2 = p;
     p2.tiles = w.tiles2, p2.n_tiles = w.counts + 1;
+    CUtensorMap map;
+    rc = make_tensor_map(&map, w.gu16, 0, 2 * static_cast<uint64_t>(a.I), plan.cols, plan.cols * 2, kBK);
+    if (rc) return rc;
     if (a.bits == 4) {
-        rc = plan.large ? launch_phase<4, 1, kLargeN1>(p, s) : launch_phase<4, 1, kSmallN>(p, s);
-        if (!rc) rc = plan.large ? launch_phase<4, 2, kLargeN2>(p2, s) : launch_phase<4, 2, kSmallN>(p2, s);
+        rc = plan.large ? launch_phase<4, 1, kLargeN1>(p, map, s) : launch_phase<4, 1, kSmallN>(p, map, s);
+        if (!rc) rc = plan.large ? launch_phase<4, 2, kLargeN2>(p2, map, s) : launch_phase<4, 2, kSmallN>(p2, map, s);
     } else {
-        rc = plan.large ? launch_phase<2, 1, kLargeN1>(p, s) : launch_phase<2, 1, kSmallN>(p, s);
-        if (!rc) rc = plan.large ? launch_phase<2, 2, kLargeN2>(p2, s) : launch_phase<2, 2, kSmallN>(p2, s);
+        rc = plan.large ? launch_phase<2, 1, kLargeN1>(p, map, s) : launch_phase<2, 1, kSmallN>(p, map, s);
+        if (!rc) rc = plan.large ? launch_phase<2, 2, kLargeN2>(p2, map, s) : launch_phase<2, 2, kSmallN>(p2, map, s);
     }
     if (rc) return rc;
     return launch_ffn_backward_gather(a, w.dxp, w.dwp, a.I / 32, w.ok, w.scale, s);

@@ -1,0 +1,32 @@
+// Tensor maps and tiled bulk copies (TMA) of the training kernels.
+#pragma once
+
+#include <cuda.h>
+
+#include "sm100.cuh"
+
+namespace moe {
+
+// A map of a row-major [rows, cols] array of 16-bit values whose copies are
+// box_rows x 64 values, written with the 128-byte swizzle (row r of a copy: 128
+// bytes, 16-byte chunk c at c ^ (r % 8)); outside the array zeros are written.
+// base 16-byte aligned, row_bytes a multiple of 16.  Returns a MOE_* status.
+int make_tensor_map(CUtensorMap *map, const void *base, int bf16, uint64_t rows, uint64_t cols, uint64_t row_bytes,
+                    uint32_t box_rows);
+
+namespace sm100 {
+
+// A box of the map at (column x, row y) to shared memory, counted on `bar`.  x
+// a multiple of 8 values.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+}  // namespace sm100
+}  // namespace moe

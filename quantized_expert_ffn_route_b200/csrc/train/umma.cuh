@@ -33,5 +33,32 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// One lane of the warp, the same one every time: 1 on it, 0 on the others.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t on;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(on));
+    return on;
+}
+// The MMA and commit wrappers of sm100.cuh for a whole warp, issued by the lane
+// whose `on` is 1: the operands stay warp-uniform, so that the compiler keeps
+// them in uniform registers, where the instructions read them; under a branch
+// on the lane it moves each of them there for every MMA (measured: 112 cycles
+// an MMA against under 60).
+__device__ __forceinline__ void mma_f16_on(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_on(uint32_t on, uint64_t *bar) {
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0; "
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_addr(bar)),
+        "r"(on)
+        : "memory");
+}
+
 }  // namespace sm100
 }  // namespace moe
