@@ -128,9 +128,9 @@ int moe_expert_ffn_backward(int bits, const void *const *expert_blobs, const int
  *   d_bias   = sum_t d_logits[t,:]     [E] fp32
  * d_logits [T,E], x [T,H] and w [E,H] are MOE_F32 | MOE_BF16; dx is dx_dtype.
  * Any of dx, d_w, d_bias may be NULL (not computed); dx may be dx_in itself
- * when dx_dtype is MOE_F32.  bf16 d_logits, x and w (of the products asked
- * for) with E and H multiples of 8 and T >= 64 run on the tensor cores, else
- * fp32 arithmetic on CUDA cores.  T = 0 writes zeros to d_w and d_bias.
+ * when dx_dtype is MOE_F32.  With the three dtypes MOE_BF16 and E a multiple
+ * of 8 the products run on the tensor cores (fp32 accumulation; d_w's sum over
+ * tokens in up to one part per SM, added in order), else in fp32 on CUDA cores.  T = 0 writes zeros to d_w and d_bias.
  * H a positive multiple of 8, 1 <= E <= 32768.  ws: at least
  * moe_router_backward_ws_size(...) bytes (may be 0: then ws may be NULL). */
 size_t moe_router_backward_ws_size(int T, int H, int E, int dl_dtype, int x_dtype, int w_dtype);

@@ -54,5 +54,8 @@ struct RouterBackward {
     unsigned *err;
 };
 int launch_router_backward_simt(const RouterBackward &a, cudaStream_t s);
+bool router_backward_tc_supported(int T, int H, int E, int dl_dtype, int x_dtype, int w_dtype);
+size_t router_backward_tc_ws_bytes(int T, int H, int E);
+int launch_router_backward_tc(const RouterBackward &a, void *ws, cudaStream_t s);
 
 }  // namespace moe

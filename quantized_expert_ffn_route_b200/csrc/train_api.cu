@@ -152,8 +152,8 @@ int moe_expert_ffn_backward(int bits, const void *const *expert_blobs, const int
 
 // ----------------------------------------------------------------- router
 size_t moe_router_backward_ws_size(int T, int H, int E, int dl_dtype, int x_dtype, int w_dtype) {
-    (void)T, (void)H, (void)E, (void)dl_dtype, (void)x_dtype, (void)w_dtype;
-    return 0;
+    if (T <= 0 || H <= 0 || E <= 0 || !router_backward_tc_supported(T, H, E, dl_dtype, x_dtype, w_dtype)) return 0;
+    return router_backward_tc_ws_bytes(T, H, E);
 }
 
 int moe_router_backward(const void *d_logits, int dl_dtype, const void *x, int x_dtype, const void *w_router,
@@ -181,7 +181,9 @@ int moe_router_backward(const void *d_logits, int dl_dtype, const void *x, int x
     if (!err) return cuda_status(cudaErrorInvalidDevice, "device error word");
     const RouterBackward a = {d_logits, x, w_router, dx_in, dx, d_w, d_bias, dl_dtype, x_dtype, w_dtype, dx_dtype,
                               T, H, E, err};
-    return launch_router_backward_simt(a, reinterpret_cast<cudaStream_t>(s));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(s);
+    if (router_backward_tc_supported(T, H, E, dl_dtype, x_dtype, w_dtype)) return launch_router_backward_tc(a, ws, st);
+    return launch_router_backward_simt(a, st);
 }
 
 }  // extern "C"
