@@ -24,9 +24,16 @@ __global__ void __launch_bounds__(kActThreads) k_act_pack8(const void *__restric
     // n8, the number of 8-value pieces, is a multiple of 4: the four lanes of
     // a block are in or out together
     const long step = static_cast<long>(gridDim.x) * kActThreads;
-    for (long i = static_cast<long>(blockIdx.x) * kActThreads + threadIdx.x; i < n8; i += step) {
+    long i = static_cast<long>(blockIdx.x) * kActThreads + threadIdx.x;
+    if (i >= n8) return;
+    float next[8];
+    load8<BF16>(x, i, next);
+    for (; i < n8; i += step) {
+        // the next piece is on its way while this one is packed
         float v[8];
-        load8<BF16>(x, i, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = next[j];
+        if (i + step < n8) load8<BF16>(x, i + step, next);
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);   // NaN above inf above all

@@ -8,11 +8,13 @@
 // needs nothing but that row: the backward kernel recomputes the three sums
 // from the row it has to read anyway, and nothing is kept between the calls.
 // Both kernels move T E 4 bytes (plus the gradient out) and are bound by that
-// at large T E, by launch latency below.
+// at large T E, by the chain load - maximum - sums - store and by launches
+// below; so the counts go without atomics and memsets (a block's part each,
+// added where they are read), the last block to end adds the rows' sums, and
+// up to 128 rows of up to 1024 experts are one block's work and one launch.
 //
 // Rows of up to 1024 experts: one warp each, the row in registers.  Longer
-// rows (a model-wide pool): one block each, two reads of the row, the second
-// one from L1 or L2.
+// rows (a model-wide pool): one block each, up to 64 entries a thread.
 #include "common.cuh"
 #include "train/train.h"
 
@@ -24,66 +26,24 @@ namespace {
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBigThreads = 512;
-constexpr int kHistMax = 8192;                    // experts counted in shared memory (32 KB)
+constexpr int kOneThreads = 1024;                 // the one-block form
+constexpr int kOneRows = 128;
+constexpr int kCountThreads = 1024;
 
-// (maximum, sum of exp(l - max), sum of f exp(l - max)) of a part of a row
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// A row's maximum, sum of exp(l - max) and sum of f exp(l - max).  fmaxf drops
+// NaN; the exponential brings it back into the sums.  A row of -inf alone has
+// m = -inf and is left out before its sums (which would be NaN) are used.
 struct Soft {
     float m, s, d;
 };
-__device__ __forceinline__ Soft soft_join(const Soft &a, const Soft &b) {
-    const float m = fmaxf(a.m, b.m);
-    // a part without a finite entry has s = d = 0 (or NaN, which stays)
-    const float ea = a.m == m ? 1.f : expf(a.m - m), eb = b.m == m ? 1.f : expf(b.m - m);
-    return {m, a.s * ea + b.s * eb, a.d * ea + b.d * eb};
-}
-// Adds N entries at a time.
-template <int N>
-__device__ __forceinline__ void soft_add(Soft &a, const float (&l)[N], const float (&f)[N]) {
-    float m = a.m;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        m = fmaxf(m, l[i]);                       // drops NaN
-        nan |= l[i] != l[i];
-    }
-    if (m == -INFINITY) {                         // nothing yet: exp(-inf - -inf) is no number
-        if (nan) a.s = a.d = NAN;
-        return;
-    }
-    const float e0 = a.m == m ? 1.f : expf(a.m - m);
-    a.s *= e0;
-    a.d *= e0;
-    a.m = m;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float e = expf(l[i] - m);
-        a.s += e;
-        a.d = fmaf(f[i], e, a.d);
-    }
-}
-__device__ __forceinline__ Soft soft_warp(Soft a) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Soft b;
-        b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-        b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-        b.d = __shfl_xor_sync(0xffffffffu, a.d, o);
-        a = soft_join(a, b);
-    }
-    return a;
-}
-// The block's join, on every thread; `part` holds one entry per warp.
-__device__ __forceinline__ Soft soft_block(Soft a, Soft *part) {
-    a = soft_warp(a);
-    const int lane = threadIdx.x & 31;
-    __syncthreads();                              // the last row's readers are done with `part`
-    if (lane == 0) part[threadIdx.x >> 5] = a;
-    __syncthreads();
-    a = lane < static_cast<int>(blockDim.x >> 5) ? part[lane] : Soft{-INFINITY, 0.f, 0.f};
-    return soft_warp(a);
-}
 
-// What one row adds: D and lse^2.  A row of -inf alone adds nothing.
+// What one row adds: D and lse^2.
 struct RowSums {
     float d;
     double z;                                     // lse of a row of the type's lowest values squares out of fp32's range
@@ -95,50 +55,114 @@ __device__ __forceinline__ RowSums row_sums(const Soft &a, unsigned *err, bool l
     return {a.d / a.s, static_cast<double>(lse) * lse};
 }
 
-__device__ __forceinline__ void block_add(float d, double z, double2 *out) {
-    // one value per warp (lane 0), summed in warp order
+// A lane's (thread's) N entries: exponentials in place, sums into s and d.  m
+// is the whole row's maximum.
+template <int N>
+__device__ __forceinline__ void soft_exps(float (&l)[N], const float (&f)[N], float m, float &s, float &d) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        // nothing but -inf (and NaN) in the row: exp(-inf - -inf) is no number
+        l[i] = m == -INFINITY ? (l[i] != l[i] ? l[i] : 0.f) : expf(l[i] - m);
+        s += l[i];
+        d = fmaf(f[i], l[i], d);
+    }
+}
+
+// The block's sum of one value a warp (lane 0's), in warp order, on thread 0.
+__device__ __forceinline__ double2 block_rows(float d, double z) {
     __shared__ double2 part[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
     if (lane == 0) part[warp] = make_double2(d, z);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double2 a = part[0];
+    double2 a = part[0];
+    if (threadIdx.x == 0)
         for (int i = 1; i < n; ++i) {
             a.x += part[i].x;
             a.y += part[i].y;
         }
-        *out = a;
+    return a;
+}
+
+struct LossOut {
+    int E;
+    float balance, z;      // coefficients
+    float *loss;
+};
+__device__ __forceinline__ void write_loss(const LossOut &o, double2 sum, int tokens) {
+    const double N = max(tokens, 1);
+    const double b = o.E * sum.x / N, z = sum.y / N;
+    o.loss[0] = static_cast<float>(o.balance * b + o.z * z);
+    o.loss[1] = static_cast<float>(b);
+    o.loss[2] = static_cast<float>(z);
+    o.loss[3] = static_cast<float>(tokens);
+}
+
+// The last block to come adds all blocks' parts, in block order.
+__device__ __forceinline__ void finish_loss(double2 mine, double2 *part, unsigned *ticket, const LossOut &o, int tokens) {
+    __shared__ bool last;
+    __shared__ double2 sum[32];
+    if (threadIdx.x == 0) {
+        part[blockIdx.x] = mine;
+        __threadfence();
+        last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double2 a = make_double2(0., 0.);
+    for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += blockDim.x) {
+        const double2 v = __ldcg(part + i);
+        a.x += v.x;
+        a.y += v.y;
+    }
+#pragma unroll
+    for (int o2 = 16; o2 > 0; o2 >>= 1) {
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, o2);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, o2);
+    }
+    if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i) {
+            a.x += sum[i].x;
+            a.y += sum[i].y;
+        }
+        write_loss(o, a, tokens);
     }
 }
-}  // namespace
 
-// counts[0..E-1] and counts[E], zero before: (token, slot) pairs and tokens.
-__global__ void __launch_bounds__(kBalThreads) k_balance_counts(const int32_t *__restrict__ ids,
-                                                                const uint8_t *__restrict__ mask, int T, int E, int k,
-                                                                int32_t *counts, unsigned *err) {
-    extern __shared__ int32_t hist[];
-    const bool local = E <= kHistMax;
-    if (local) {
-        for (int e = threadIdx.x; e < E; e += kBalThreads) hist[e] = 0;
-        __syncthreads();
-    }
+// Counts this block's share of the (token, slot) pairs into hist [E + 1] (in
+// shared memory, zeroed), the last entry the tokens.
+__device__ __forceinline__ void count_pairs(const int32_t *ids, const uint8_t *mask, int T, int E, int k, int part,
+                                            int parts, int32_t *hist, unsigned *err) {
     const int n = T * k;
     int tokens = 0;
-    for (int i = blockIdx.x * kBalThreads + threadIdx.x; i < n; i += gridDim.x * kBalThreads) {
+    for (int i = part * blockDim.x + threadIdx.x; i < n; i += parts * blockDim.x) {
         const int t = i / k;
         if (mask && !mask[t]) continue;
         tokens += i == t * k;
         const int e = ids[i];
         if (e < 0 || e >= E) report(err, MOE_DEVERR_BAD_EXPERT);
-        else atomicAdd((local ? hist : counts) + e, 1);
+        else atomicAdd(hist + e, 1);
     }
     tokens = __reduce_add_sync(0xffffffffu, tokens);
-    if ((threadIdx.x & 31) == 0 && tokens) atomicAdd(counts + E, tokens);
-    if (local) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < E; e += kBalThreads)
-            if (hist[e]) atomicAdd(counts + e, hist[e]);
-    }
+    if ((threadIdx.x & 31) == 0 && tokens) atomicAdd(hist + E, tokens);
+}
+}  // namespace
+
+// counts [parts, E + 1]: each block's part (one block: the counts themselves).
+__global__ void __launch_bounds__(kCountThreads) k_balance_counts(const int32_t *__restrict__ ids,
+                                                                  const uint8_t *__restrict__ mask, int T, int E, int k,
+                                                                  int32_t *__restrict__ counts, unsigned *ticket,
+                                                                  unsigned *err) {
+    extern __shared__ int32_t hist[];
+    for (int e = threadIdx.x; e <= E; e += kCountThreads) hist[e] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+    __syncthreads();
+    count_pairs(ids, mask, T, E, k, blockIdx.x, gridDim.x, hist, err);
+    __syncthreads();
+    int32_t *out = counts + static_cast<size_t>(blockIdx.x) * (E + 1);
+    for (int e = threadIdx.x; e <= E; e += kCountThreads) out[e] = hist[e];
 }
 
 // Four neighbouring entries of a row from column c on (fill beyond E).
@@ -170,91 +194,128 @@ __device__ __forceinline__ void share4(const int32_t *counts, int c, int E, floa
     for (int i = 0; i < 4; ++i) f[i] = c + i < E ? counts[c + i] * unit : 0.f;
 }
 
-// One warp per row, NV float4 per lane (E <= 128 NV).
+// The sums of one row by a warp, NV float4 per lane (E <= 128 NV).
 template <int NV, bool VEC>
-__global__ void __launch_bounds__(kBalThreads) k_balance_rows(const float *__restrict__ logits,
-                                                              const uint8_t *__restrict__ mask, int T, int E, int k,
-                                                              const int32_t *__restrict__ counts,
-                                                              double2 *__restrict__ part, unsigned *err) {
+__device__ __forceinline__ Soft warp_row(const float *row, int E, const float (&f)[NV][4], float (&l)[NV][4]) {
     const int lane = threadIdx.x & 31;
-    const float unit = 1.f / (static_cast<float>(max(counts[E], 1)) * k);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) row4<VEC>(row, 4 * lane + 128 * i, E, -INFINITY, l[i]);
+    Soft a = {-INFINITY, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) a.m = fmaxf(a.m, fmaxf(fmaxf(l[i][0], l[i][1]), fmaxf(l[i][2], l[i][3])));
+    a.m = warp_max(a.m);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) soft_exps(l[i], f[i], a.m, a.s, a.d);
+    a.s = warp_sum(a.s);
+    a.d = warp_sum(a.d);
+    return a;
+}
+
+// Rows r0, r0 + step, .. by this warp: their D and lse^2 added up.
+template <int NV, bool VEC>
+__device__ __forceinline__ RowSums warp_rows(const float *logits, const uint8_t *mask, int T, int E, float unit,
+                                             const int32_t *counts, int r0, int step, unsigned *err) {
+    const int lane = threadIdx.x & 31;
     float f[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) share4<VEC>(counts, 4 * lane + 128 * i, E, unit, f[i]);
-    float sd = 0.f;
-    double sz = 0.;
-    for (int t = blockIdx.x * kBalWarps + (threadIdx.x >> 5); t < T; t += gridDim.x * kBalWarps) {
+    RowSums sum = {0.f, 0.};
+    for (int t = r0; t < T; t += step) {
         if (mask && !mask[t]) continue;
-        const float *row = logits + static_cast<size_t>(t) * E;
         float l[NV][4];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) row4<VEC>(row, 4 * lane + 128 * i, E, -INFINITY, l[i]);
-        Soft a = {-INFINITY, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < NV; ++i) soft_add(a, l[i], f[i]);
-        const RowSums r = row_sums(soft_warp(a), err, lane == 0);
-        sd += r.d;
-        sz += r.z;
+        const RowSums r = row_sums(warp_row<NV, VEC>(logits + static_cast<size_t>(t) * E, E, f, l), err, lane == 0);
+        sum.d += r.d;
+        sum.z += r.z;
     }
-    block_add(sd, sz, part + blockIdx.x);
+    return sum;
 }
 
-// One block per row.
-template <bool VEC>
+// Rows of up to 1024 experts, the counts' parts added first.
+template <int NV, bool VEC>
+__global__ void __launch_bounds__(kBalThreads) k_balance_rows(const float *__restrict__ logits,
+                                                              const uint8_t *__restrict__ mask, int T, int E, int k,
+                                                              const int32_t *__restrict__ parts, int n_parts,
+                                                              int32_t *__restrict__ counts, double2 *part,
+                                                              unsigned *ticket, LossOut o, unsigned *err) {
+    __shared__ __align__(16) int32_t n[1024 + 4];
+    for (int e = threadIdx.x; e <= E; e += kBalThreads) {
+        int c = 0;
+        for (int p = 0; p < n_parts; ++p) c += parts[static_cast<size_t>(p) * (E + 1) + e];
+        n[e] = c;
+        if (blockIdx.x == 0) counts[e] = c;
+    }
+    __syncthreads();
+    const float unit = 1.f / (static_cast<float>(max(n[E], 1)) * k);
+    const RowSums r = warp_rows<NV, VEC>(logits, mask, T, E, unit, n, blockIdx.x * kBalWarps + (threadIdx.x >> 5),
+                                         gridDim.x * kBalWarps, err);
+    finish_loss(block_rows(r.d, r.z), part, ticket, o, n[E]);
+}
+
+// Few rows of up to 1024 experts: counts, rows and losses by one block.
+template <int NV, bool VEC>
+__global__ void __launch_bounds__(kOneThreads) k_balance_one(const float *__restrict__ logits,
+                                                             const int32_t *__restrict__ ids,
+                                                             const uint8_t *__restrict__ mask, int T, int E, int k,
+                                                             int32_t *__restrict__ counts, LossOut o, unsigned *err) {
+    __shared__ __align__(16) int32_t n[1024 + 4];
+    for (int e = threadIdx.x; e <= E; e += kOneThreads) n[e] = 0;
+    __syncthreads();
+    count_pairs(ids, mask, T, E, k, 0, 1, n, err);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= E; e += kOneThreads) counts[e] = n[e];
+    const float unit = 1.f / (static_cast<float>(max(n[E], 1)) * k);
+    const RowSums r = warp_rows<NV, VEC>(logits, mask, T, E, unit, n, threadIdx.x >> 5, kOneThreads / 32, err);
+    const double2 sum = block_rows(r.d, r.z);
+    if (threadIdx.x == 0) write_loss(o, sum, n[E]);
+}
+
+// The sums of one row by a block, V float4 per thread (E <= 2048 V); on every thread.
+template <int V, bool VEC>
+__device__ __forceinline__ Soft block_row(const float *row, int E, const int32_t *counts, float unit, float (&l)[V][4],
+                                          float (&f)[V][4]) {
+    __shared__ float red[3][kBigThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < V; ++i) row4<VEC>(row, 4 * (threadIdx.x + kBigThreads * i), E, -INFINITY, l[i]);
+    Soft a = {-INFINITY, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.m = fmaxf(a.m, fmaxf(fmaxf(l[i][0], l[i][1]), fmaxf(l[i][2], l[i][3])));
+    a.m = warp_max(a.m);
+    __syncthreads();                              // the last row's values are read
+    if (lane == 0) red[0][warp] = a.m;
+    __syncthreads();
+    a.m = warp_max(lane < kBigThreads / 32 ? red[0][lane] : -INFINITY);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        share4<VEC>(counts, 4 * (threadIdx.x + kBigThreads * i), E, unit, f[i]);
+        soft_exps(l[i], f[i], a.m, a.s, a.d);
+    }
+    a.s = warp_sum(a.s);
+    a.d = warp_sum(a.d);
+    if (lane == 0) red[1][warp] = a.s, red[2][warp] = a.d;
+    __syncthreads();
+    a.s = warp_sum(lane < kBigThreads / 32 ? red[1][lane] : 0.f);
+    a.d = warp_sum(lane < kBigThreads / 32 ? red[2][lane] : 0.f);
+    return a;
+}
+
+template <int V, bool VEC>
 __global__ void __launch_bounds__(kBigThreads) k_balance_rows_big(const float *__restrict__ logits,
                                                                   const uint8_t *__restrict__ mask, int T, int E,
                                                                   int k, const int32_t *__restrict__ counts,
-                                                                  double2 *__restrict__ part, unsigned *err) {
-    __shared__ Soft warps[kBigThreads / 32];
+                                                                  double2 *part, unsigned *ticket, LossOut o,
+                                                                  unsigned *err) {
     const float unit = 1.f / (static_cast<float>(max(counts[E], 1)) * k);
-    float sd = 0.f;
-    double sz = 0.;
+    RowSums sum = {0.f, 0.};
     for (int t = blockIdx.x; t < T; t += gridDim.x) {
         if (mask && !mask[t]) continue;
-        const float *row = logits + static_cast<size_t>(t) * E;
-        Soft a = {-INFINITY, 0.f, 0.f};
-        for (int c = 4 * threadIdx.x; c < E; c += 4 * kBigThreads) {
-            float l[4], f[4];
-            row4<VEC>(row, c, E, -INFINITY, l);
-            share4<VEC>(counts, c, E, unit, f);
-            soft_add(a, l, f);
-        }
-        const RowSums r = row_sums(soft_block(a, warps), err, threadIdx.x == 0);
-        if (threadIdx.x == 0) {
-            sd += r.d;
-            sz += r.z;
-        }
+        float l[V][4], f[V][4];
+        const RowSums r = row_sums(block_row<V, VEC>(logits + static_cast<size_t>(t) * E, E, counts, unit, l, f), err,
+                                   threadIdx.x == 0);
+        sum.d += r.d;
+        sum.z += r.z;
     }
-    block_add(threadIdx.x == 0 ? sd : 0.f, threadIdx.x == 0 ? sz : 0., part + blockIdx.x);
-}
-
-// Sums the blocks' parts in a fixed order and writes the four losses.
-__global__ void __launch_bounds__(256) k_balance_finish(const double2 *__restrict__ part, int n,
-                                                        const int32_t *__restrict__ counts, int E, float balance_coef,
-                                                        float z_coef, float *__restrict__ loss) {
-    __shared__ double2 sum[256];
-    double2 a = make_double2(0., 0.);
-    for (int i = threadIdx.x; i < n; i += 256) {
-        a.x += part[i].x;
-        a.y += part[i].y;
-    }
-    sum[threadIdx.x] = a;
-    __syncthreads();
-    for (int o = 128; o > 0; o >>= 1) {
-        if (threadIdx.x < o) {
-            sum[threadIdx.x].x += sum[threadIdx.x + o].x;
-            sum[threadIdx.x].y += sum[threadIdx.x + o].y;
-        }
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) {
-        const double N = max(counts[E], 1);
-        const double b = E * sum[0].x / N, z = sum[0].y / N;
-        loss[0] = static_cast<float>(balance_coef * b + z_coef * z);
-        loss[1] = static_cast<float>(b);
-        loss[2] = static_cast<float>(z);
-        loss[3] = static_cast<float>(counts[E]);
-    }
+    finish_loss(make_double2(sum.d, sum.z), part, ticket, o, counts[E]);
 }
 
 // ---------------------------------------------------------------- backward
@@ -307,33 +368,42 @@ __device__ __forceinline__ RowGrad row_grad(const Soft &a, float gb, float gc, u
     if (leader && !isfinite(lse)) report(err, MOE_DEVERR_NONFINITE);
     return {a.m, 1.f / a.s, gb, gc * lse - gb * (a.d / a.s)};
 }
-__device__ __forceinline__ float loss_term(const RowGrad &r, float l, float f) {
-    return expf(l - r.m) * r.inv_s * fmaf(r.alpha, f, r.beta);
+__device__ __forceinline__ float loss_term(const RowGrad &r, float e, float f) {
+    return e * r.inv_s * fmaf(r.alpha, f, r.beta);
+}
+
+// Lane j < k's slot of a token, read before the row is.
+struct Slot {
+    int id;
+    float w, dw;
+};
+__device__ __forceinline__ Slot slot_of(const RouteGrad &a, int t, bool on) {
+    const int lane = threadIdx.x & 31;
+    const bool in = on && a.dw && lane < a.k;
+    const size_t at = static_cast<size_t>(t) * a.k + lane;
+    return {in ? a.ids[at] : -1, in ? a.w[at] : 0.f, in ? a.dw[at] : 0.f};
 }
 
 // The gates' gradient: lane j < k writes the whole entry of its expert, the
 // loss term included (equal ids write equal values).  The row is written.
 template <bool BF16, bool LOSS>
-__device__ __forceinline__ void gate_entries(const RouteGrad &a, int t, const RowGrad &r, float unit) {
+__device__ __forceinline__ void gate_entries(const RouteGrad &a, int t, const Slot &s, const RowGrad &r, float unit) {
     const int lane = threadIdx.x & 31;
-    const size_t at = static_cast<size_t>(t) * a.k + lane;
-    const bool in = lane < a.k;
-    const int id = in ? a.ids[at] : -1;
-    const float w = in ? a.w[at] : 0.f, dw = in ? a.dw[at] : 0.f;
-    const float mean = warp_sum(in ? w * dw : 0.f);
-    const float mine = w * (dw - mean);
+    const bool in = lane < a.k, good = in && s.id >= 0 && s.id < a.E;
+    const size_t at = static_cast<size_t>(t) * a.E + (good ? s.id : 0);
+    float l = 0.f, n = 0.f;
+    if (LOSS && good) l = a.logits[at], n = a.counts[s.id] * unit;
+    const float mean = warp_sum(in ? s.w * s.dw : 0.f);
+    const float mine = s.w * (s.dw - mean);
     float g = 0.f;
     for (int j = 0; j < a.k; ++j) {
         const float v = __shfl_sync(0xffffffffu, mine, j);
-        if (__shfl_sync(0xffffffffu, id, j) == id) g += v;
+        if (__shfl_sync(0xffffffffu, s.id, j) == s.id) g += v;
     }
-    if (!in) return;
-    if (id < 0 || id >= a.E) {
-        report(a.err, MOE_DEVERR_BAD_EXPERT);
-        return;
-    }
-    if constexpr (LOSS) g += loss_term(r, a.logits[static_cast<size_t>(t) * a.E + id], a.counts[id] * unit);
-    put1<BF16>(a.dl, static_cast<size_t>(t) * a.E + id, g);
+    if (in && !good) report(a.err, MOE_DEVERR_BAD_EXPERT);
+    if (!good) return;
+    if constexpr (LOSS) g += loss_term(r, r.alpha == 0.f && r.inv_s == 0.f ? 0.f : expf(l - r.m), n);
+    put1<BF16>(a.dl, at, g);
 }
 
 // One warp per row, NV float4 per lane.
@@ -349,41 +419,31 @@ __global__ void __launch_bounds__(kBalThreads) k_route_backward(RouteGrad a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) share4<VEC>(a.counts, 4 * lane + 128 * i, a.E, unit, f[i]);
     }
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     for (int t = blockIdx.x * kBalWarps + (threadIdx.x >> 5); t < a.T; t += gridDim.x * kBalWarps) {
         const size_t row = static_cast<size_t>(t) * a.E;
         const bool on = !a.mask || a.mask[t];
+        const Slot slot = slot_of(a, t, on);
         RowGrad r = {0.f, 0.f, 0.f, 0.f};
+        float v[NV][4] = {};
         if (LOSS && on) {
-            float l[NV][4];
+            r = row_grad(warp_row<NV, VEC>(a.logits + row, a.E, f, v), gb, gc, a.err, lane == 0);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) row4<VEC>(a.logits + row, 4 * lane + 128 * i, a.E, -INFINITY, l[i]);
-            Soft s = {-INFINITY, 0.f, 0.f};
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) soft_add(s, l[i], f[i]);
-            r = row_grad(soft_warp(s), gb, gc, a.err, lane == 0);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = loss_term(r, l[i][j], f[i][j]);
-                put4<BF16, VEC>(a.dl, row, 4 * lane + 128 * i, a.E, v);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) put4<BF16, VEC>(a.dl, row, 4 * lane + 128 * i, a.E, zero);
+                for (int j = 0; j < 4; ++j) v[i][j] = loss_term(r, v[i][j], f[i][j]);
         }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) put4<BF16, VEC>(a.dl, row, 4 * lane + 128 * i, a.E, v[i]);
         if (on && a.dw) {
             __syncwarp();                          // the row is written before its entries are
-            gate_entries<BF16, LOSS>(a, t, r, unit);
+            gate_entries<BF16, LOSS>(a, t, slot, r, unit);
         }
     }
 }
 
-// One block per row.
-template <bool VEC, bool BF16, bool LOSS>
+// One block per row, V float4 per thread.
+template <int V, bool VEC, bool BF16, bool LOSS>
 __global__ void __launch_bounds__(kBigThreads) k_route_backward_big(RouteGrad a) {
-    __shared__ Soft warps[kBigThreads / 32];
     float gb = 0.f, gc = 0.f, unit = 0.f;
     if constexpr (LOSS) {
         const float n = static_cast<float>(max(a.counts[a.E], 1)), g = a.d_loss ? *a.d_loss : 1.f;
@@ -391,33 +451,24 @@ __global__ void __launch_bounds__(kBigThreads) k_route_backward_big(RouteGrad a)
         gb = g * a.balance * a.E / n;
         gc = g * a.z * 2.f / n;
     }
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
         const size_t row = static_cast<size_t>(t) * a.E;
         const bool on = !a.mask || a.mask[t];
+        const Slot slot = slot_of(a, t, on && threadIdx.x < 32);
         RowGrad r = {0.f, 0.f, 0.f, 0.f};
+        float v[V][4] = {};
         if (LOSS && on) {
-            Soft s = {-INFINITY, 0.f, 0.f};
-            for (int c = 4 * threadIdx.x; c < a.E; c += 4 * kBigThreads) {
-                float l[4], f[4];
-                row4<VEC>(a.logits + row, c, a.E, -INFINITY, l);
-                share4<VEC>(a.counts, c, a.E, unit, f);
-                soft_add(s, l, f);
-            }
-            r = row_grad(soft_block(s, warps), gb, gc, a.err, threadIdx.x == 0);
-            for (int c = 4 * threadIdx.x; c < a.E; c += 4 * kBigThreads) {
-                float l[4], f[4], v[4];
-                row4<VEC>(a.logits + row, c, a.E, -INFINITY, l);
-                share4<VEC>(a.counts, c, a.E, unit, f);
+            float f[V][4];
+            r = row_grad(block_row<V, VEC>(a.logits + row, a.E, a.counts, unit, v, f), gb, gc, a.err, threadIdx.x == 0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = loss_term(r, l[j], f[j]);
-                put4<BF16, VEC>(a.dl, row, c, a.E, v);
-            }
-        } else {
-            for (int c = 4 * threadIdx.x; c < a.E; c += 4 * kBigThreads) put4<BF16, VEC>(a.dl, row, c, a.E, zero);
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = loss_term(r, v[i][j], f[i][j]);
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) put4<BF16, VEC>(a.dl, row, 4 * (threadIdx.x + kBigThreads * i), a.E, v[i]);
         __syncthreads();                           // the row is written before its entries are
-        if (on && a.dw && threadIdx.x < 32) gate_entries<BF16, LOSS>(a, t, r, unit);
+        if (on && a.dw && threadIdx.x < 32) gate_entries<BF16, LOSS>(a, t, slot, r, unit);
     }
 }
 
@@ -427,74 +478,119 @@ static int row_blocks(int T) {
     return static_cast<int>(want < cap ? want : cap);
 }
 static int big_blocks(int T) {
-    const int cap = num_sms() * 3;
+    const int cap = num_sms() * 2;
     return T < cap ? T : cap;
 }
+// Blocks that count: up to eight while their parts are few numbers to add (up
+// to 1024 experts), each with at least 4096 pairs.
+static int count_parts(int T, int E, int k) {
+    if (E > 1024) return 1;
+    const long n = (static_cast<long>(T) * k + 4095) / 4096;
+    return static_cast<int>(n < 1 ? 1 : n < 8 ? n : 8);
+}
 
-size_t balance_ws_bytes(int T, int E) {
-    return static_cast<size_t>(E <= 1024 ? row_blocks(T) : big_blocks(T)) * sizeof(double2);
+struct BalanceWs {
+    unsigned *ticket;
+    double2 *part;
+    int32_t *counts;
+};
+static size_t carve(int T, int E, uint8_t *base, BalanceWs *out) {
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        uint8_t *p = base ? base + at : nullptr;
+        at += (n + 255) / 256 * 256;
+        return p;
+    };
+    BalanceWs w;
+    w.ticket = reinterpret_cast<unsigned *>(take(sizeof(unsigned)));
+    w.part = reinterpret_cast<double2 *>(take((E <= 1024 ? row_blocks(T) : big_blocks(T)) * sizeof(double2)));
+    w.counts = reinterpret_cast<int32_t *>(take(E <= 1024 ? 8 * (static_cast<size_t>(E) + 1) * 4 : 0));
+    if (out) *out = w;
+    return at;
+}
+size_t balance_ws_bytes(int T, int E) { return carve(T, E, nullptr, nullptr); }
+
+// The instantiation for E <= 1024: float4 per lane, whether rows are aligned.
+template <class F>
+static void by_row(int E, F &&go) {
+    using std::integral_constant;
+    auto v = [&](auto nv) {
+        if (E % 4 == 0) go(nv, std::true_type{});
+        else go(nv, std::false_type{});
+    };
+    if (E <= 128) v(integral_constant<int, 1>{});
+    else if (E <= 256) v(integral_constant<int, 2>{});
+    else if (E <= 512) v(integral_constant<int, 4>{});
+    else v(integral_constant<int, 8>{});
+}
+// And above: float4 per thread.
+template <class F>
+static void by_big_row(int E, F &&go) {
+    using std::integral_constant;
+    auto v = [&](auto nv) {
+        if (E % 4 == 0) go(nv, std::true_type{});
+        else go(nv, std::false_type{});
+    };
+    if (E <= 2048 * 4) v(integral_constant<int, 4>{});
+    else if (E <= 2048 * 8) v(integral_constant<int, 8>{});
+    else v(integral_constant<int, 16>{});
 }
 
 int launch_balance_loss(const float *logits, const int32_t *ids, const uint8_t *mask, int T, int E, int k,
                         float balance_coef, float z_coef, int32_t *counts, float *loss, void *ws, unsigned *err,
                         cudaStream_t s) {
-    int rc = cuda_status(cudaMemsetAsync(counts, 0, (static_cast<size_t>(E) + 1) * sizeof(int32_t), s), "counts memset");
+    BalanceWs w;
+    carve(T, E, static_cast<uint8_t *>(ws), &w);
+    const LossOut o = {E, balance_coef, z_coef, loss};
+    if (E <= 1024 && T <= kOneRows) {
+        by_row(E, [&](auto nv, auto vec) {
+            k_balance_one<decltype(nv)::value, decltype(vec)::value>
+                <<<1, kOneThreads, 0, s>>>(logits, ids, mask, T, E, k, counts, o, err);
+        });
+        count_launches(1);
+        return cuda_status(cudaGetLastError(), "balance loss launch");
+    }
+    const int parts = count_parts(T, E, k);
+    const size_t smem = (static_cast<size_t>(E) + 1) * sizeof(int32_t);
+    int rc = cuda_status(cudaFuncSetAttribute(k_balance_counts, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              static_cast<int>(smem)),
+                         "balance smem attribute");
     if (rc) return rc;
-    double2 *part = static_cast<double2 *>(ws);
-    const long pairs = static_cast<long>(T) * k;
-    long blocks = (pairs + 8L * kBalThreads - 1) / (8L * kBalThreads);
-    if (blocks > num_sms()) blocks = num_sms();
-    k_balance_counts<<<blocks, kBalThreads, E <= kHistMax ? E * sizeof(int32_t) : 0, s>>>(ids, mask, T, E, k, counts,
-                                                                                          err);
-    const int n = E <= 1024 ? row_blocks(T) : big_blocks(T);
-    const bool vec = E % 4 == 0;
-    if (E > 1024) {
-        if (vec) k_balance_rows_big<true><<<n, kBigThreads, 0, s>>>(logits, mask, T, E, k, counts, part, err);
-        else k_balance_rows_big<false><<<n, kBigThreads, 0, s>>>(logits, mask, T, E, k, counts, part, err);
-    } else {
-#define MOE_ROWS(NV)                                                                                            \
-    do {                                                                                                        \
-        if (vec) k_balance_rows<NV, true><<<n, kBalThreads, 0, s>>>(logits, mask, T, E, k, counts, part, err);  \
-        else k_balance_rows<NV, false><<<n, kBalThreads, 0, s>>>(logits, mask, T, E, k, counts, part, err);     \
-    } while (0)
-        if (E <= 128) MOE_ROWS(1);
-        else if (E <= 256) MOE_ROWS(2);
-        else if (E <= 512) MOE_ROWS(4);
-        else MOE_ROWS(8);
-#undef MOE_ROWS
-    }
-    k_balance_finish<<<1, 256, 0, s>>>(part, n, counts, E, balance_coef, z_coef, loss);
-    count_launches(3);
+    k_balance_counts<<<parts, kCountThreads, smem, s>>>(ids, mask, T, E, k, E <= 1024 ? w.counts : counts, w.ticket, err);
+    if (E <= 1024)
+        by_row(E, [&](auto nv, auto vec) {
+            k_balance_rows<decltype(nv)::value, decltype(vec)::value><<<row_blocks(T), kBalThreads, 0, s>>>(
+                logits, mask, T, E, k, w.counts, parts, counts, w.part, w.ticket, o, err);
+        });
+    else
+        by_big_row(E, [&](auto nv, auto vec) {
+            k_balance_rows_big<decltype(nv)::value, decltype(vec)::value><<<big_blocks(T), kBigThreads, 0, s>>>(
+                logits, mask, T, E, k, counts, w.part, w.ticket, o, err);
+        });
+    count_launches(2);
     return cuda_status(cudaGetLastError(), "balance loss launch");
-}
-
-template <bool BF16, bool LOSS, bool VEC>
-static void route_backward_rows(const RouteGrad &a, cudaStream_t s) {
-    if (a.E > 1024) {
-        k_route_backward_big<VEC, BF16, LOSS><<<big_blocks(a.T), kBigThreads, 0, s>>>(a);
-        return;
-    }
-    const int n = row_blocks(a.T);
-    if (a.E <= 128) k_route_backward<1, VEC, BF16, LOSS><<<n, kBalThreads, 0, s>>>(a);
-    else if (a.E <= 256) k_route_backward<2, VEC, BF16, LOSS><<<n, kBalThreads, 0, s>>>(a);
-    else if (a.E <= 512) k_route_backward<4, VEC, BF16, LOSS><<<n, kBalThreads, 0, s>>>(a);
-    else k_route_backward<8, VEC, BF16, LOSS><<<n, kBalThreads, 0, s>>>(a);
 }
 
 int launch_route_backward(const float *logits, const int32_t *ids, const float *w, const float *dw,
                           const uint8_t *mask, const int32_t *counts, const float *d_loss, int T, int E, int k,
                           float balance_coef, float z_coef, void *dl, int dl_dtype, unsigned *err, cudaStream_t s) {
     const RouteGrad a = {logits, ids, w, dw, mask, counts, d_loss, T, E, k, balance_coef, z_coef, dl, err};
-    const bool bf16 = dl_dtype == MOE_BF16, loss = counts != nullptr, vec = E % 4 == 0;
-    auto go = [&](auto b, auto l) {
-        constexpr bool B = decltype(b)::value, L = decltype(l)::value;
-        if (vec) route_backward_rows<B, L, true>(a, s);
-        else route_backward_rows<B, L, false>(a, s);
+    auto go = [&](auto bf16, auto with_loss) {
+        constexpr bool B = decltype(bf16)::value, L = decltype(with_loss)::value;
+        if (E <= 1024)
+            by_row(E, [&](auto nv, auto vec) {
+                k_route_backward<decltype(nv)::value, decltype(vec)::value, B, L><<<row_blocks(T), kBalThreads, 0, s>>>(a);
+            });
+        else
+            by_big_row(E, [&](auto nv, auto vec) {
+                k_route_backward_big<decltype(nv)::value, decltype(vec)::value, B, L>
+                    <<<big_blocks(T), kBigThreads, 0, s>>>(a);
+            });
     };
     using Yes = std::true_type;
     using No = std::false_type;
-    if (bf16) loss ? go(Yes{}, Yes{}) : go(Yes{}, No{});
-    else loss ? go(No{}, Yes{}) : go(No{}, No{});
+    if (dl_dtype == MOE_BF16) counts ? go(Yes{}, Yes{}) : go(Yes{}, No{});
+    else counts ? go(No{}, Yes{}) : go(No{}, No{});
     count_launches(1);
     return cuda_status(cudaGetLastError(), "route backward launch");
 }

@@ -13,143 +13,185 @@ import ctypes as C
 
 MOE_Q8 = 2          # activation given as an 8-bit checkpoint (codes, scales)
 
-_P, _I, _F, _Z = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+_PTR, _INT, _FLT, _SZ = C.c_void_p, C.c_int, C.c_float, C.c_size_t
 SIGNATURES = {
-    "moe_act_pack8": (_I, [_P, _I, _I, _I, _P, _P, _P]),
-    "moe_act_unpack8": (_I, [_P, _P, _I, _I, _P, _I, _P]),
-    "moe_balance_ws_size": (_Z, [_I, _I]),
-    "moe_balance_loss": (_I, [_P, _P, _P, _I, _I, _I, _F, _F, _P, _P, _P, _Z, _P]),
-    "moe_route_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _F, _F, _P, _I, _P]),
-    "moe_expert_ffn_backward_ws_size": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
-    "moe_expert_ffn_backward": (_I, [_I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I,
-                                     _P, _I, _P, _Z, _P]),
-    "moe_router_backward_ws_size": (_Z, [_I, _I, _I, _I, _I, _I]),
-    "moe_router_backward": (_I, [_P, _I, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _Z, _P]),
+    "moe_act_pack8": (_INT, [_PTR, _INT, _INT, _INT, _PTR, _PTR, _PTR]),
+    "moe_act_unpack8": (_INT, [_PTR, _PTR, _INT, _INT, _PTR, _INT, _PTR]),
+    "moe_balance_ws_size": (_SZ, [_INT, _INT]),
+    "moe_balance_loss": (_INT, [_PTR, _PTR, _PTR, _INT, _INT, _INT, _FLT, _FLT, _PTR, _PTR, _PTR, _SZ, _PTR]),
+    "moe_route_backward": (_INT, [_PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _INT, _INT, _INT, _FLT, _FLT, _PTR, _INT, _PTR]),
+    "moe_expert_ffn_backward_ws_size": (_SZ, [_INT, _INT, _INT, _INT, _INT, _INT, _INT]),
+    "moe_expert_ffn_backward": (_INT, [_INT, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _INT, _PTR, _PTR, _INT, _INT, _INT, _INT, _INT, _INT, _PTR, _PTR, _INT,
+                                     _PTR, _INT, _PTR, _SZ, _PTR]),
+    "moe_router_backward_ws_size": (_SZ, [_INT, _INT, _INT, _INT, _INT, _INT]),
+    "moe_router_backward": (_INT, [_PTR, _INT, _PTR, _INT, _PTR, _INT, _PTR, _INT, _INT, _INT, _PTR, _INT, _PTR, _PTR, _PTR, _SZ, _PTR]),
 }
 
 
-class _Call:
-    """Checks one call's tensors and runs it on their device."""
+# A call's checks and marshalling are most of a small call's time on the host:
+# the good case of _p is five attribute reads, and everything that can be looked
+# up once is.
+_lib = _current = _raw_stream = None        # the library; the current device; a device's current stream
+_T = {}                                     # dtype code -> torch types
 
-    def __init__(self, name):
-        self.name, self.device = name, None
 
-    def ptr(self, t, what, dtypes, count):
-        """Pointer of a buffer of at least `count` values; None and integers pass."""
-        if t is None or isinstance(t, int):
-            return t
+def _load():
+    """First call: the library and what the checks need of torch."""
+    global _lib, _current, _raw_stream
+    import torch
+    from . import lib
+    f32, bf16, i8 = torch.float32, torch.bfloat16, torch.int8
+    _T.update({0: (f32,), 1: (bf16,), MOE_Q8: (i8,), "i32": (torch.int32,), "i64": (torch.int64,),
+               "u8": (torch.uint8,), "mask": (torch.uint8, torch.bool), None: (f32, bf16, i8)})
+    _current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _lib = lib()
+    return _lib
+
+
+def _any(code):
+    """torch types of a dtype argument (an unknown code passes: the C call refuses it)."""
+    return _T.get(code) or _T[None]
+
+
+def _p(dev, name, what, t, types, count):
+    """(device, pointer) of a buffer of at least `count` values of one of `types`;
+    None and addresses pass.  dev: the device of the buffers before it, or None."""
+    if t is None:
+        return dev, None
+    try:
+        d = t.get_device()
+        if t.dtype in types and (d == dev or dev is None) and d >= 0 and t.is_contiguous() and t.numel() >= count:
+            return d, t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, int):
+        return dev, t
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: {what} must be a CUDA tensor, an address or None (got {type(t).__name__})")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: {what} must be a CUDA tensor (got {t.device})")
+    if t.dtype not in types:
+        raise ValueError(f"{name}: {what} has type {t.dtype}, expected {' or '.join(map(str, types))}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: {what} must be contiguous")
+    if t.numel() < count:
+        raise ValueError(f"{name}: {what} holds {t.numel()} values, needs {count}")
+    raise ValueError(f"{name}: {what} is on {t.device}, other buffers on cuda:{dev}")
+
+
+def _run(fn, dev, stream, *args):
+    """Calls fn(*args, stream) on the buffers' device."""
+    here = _current()
+    if dev is None or dev == here:
+        rc = fn(*args, _raw_stream(here) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream)
+    else:
         import torch
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{self.name}: {what} must be a CUDA tensor, an address or None (got {type(t).__name__})")
-        if not t.is_cuda:
-            raise ValueError(f"{self.name}: {what} must be a CUDA tensor (got {t.device})")
-        if t.dtype not in dtypes:
-            raise ValueError(f"{self.name}: {what} has type {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-        if not t.is_contiguous():
-            raise ValueError(f"{self.name}: {what} must be contiguous")
-        if t.numel() < count:
-            raise ValueError(f"{self.name}: {what} holds {t.numel()} values, needs {count}")
-        if self.device is None:
-            self.device = t.device
-        elif self.device != t.device:
-            raise ValueError(f"{self.name}: {what} is on {t.device}, other buffers on {self.device}")
-        return t.data_ptr()
-
-    def run(self, stream, *args):
-        from . import _check, _stream, lib
-        import torch
-        fn = getattr(lib(), self.name)
-        if self.device is None or self.device.index == torch.cuda.current_device():
-            return _check(fn(*args, _stream(stream)))
-        with torch.cuda.device(self.device):
-            return _check(fn(*args, _stream(stream)))
-
-
-_TYPES = None
-
-
-def _types(code):
-    """torch types of a dtype code (an unknown code passes: the C call refuses it)."""
-    global _TYPES
-    if _TYPES is None:
-        import torch
-        _TYPES = {0: (torch.float32,), 1: (torch.bfloat16,), MOE_Q8: (torch.int8,), "i32": (torch.int32,),
-                  "i64": (torch.int64,), "u8": (torch.uint8,), "mask": (torch.uint8, torch.bool),
-                  None: (torch.float32, torch.bfloat16, torch.int8)}
-    return _TYPES.get(code, _TYPES[None])
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream)
+    if rc:
+        from . import _check
+        _check(rc)
+    return rc
 
 
 def moe_act_pack8(x, x_dtype, T, H, codes, scales, stream=None):
-    c = _Call("moe_act_pack8")
-    return c.run(stream, c.ptr(x, "x", _types(x_dtype), T * H), x_dtype, T, H,
-                 c.ptr(codes, "codes", _types(MOE_Q8), T * H), c.ptr(scales, "scales", _types("u8"), T * (H // 32)))
+    f = (_lib or _load()).moe_act_pack8
+    n = "moe_act_pack8"
+    d, x = _p(None, n, "x", x, _any(x_dtype), T * H)
+    d, codes = _p(d, n, "codes", codes, _T[MOE_Q8], T * H)
+    d, scales = _p(d, n, "scales", scales, _T["u8"], T * (H // 32))
+    return _run(f, d, stream, x, x_dtype, T, H, codes, scales)
 
 
 def moe_act_unpack8(codes, scales, T, H, x, x_dtype, stream=None):
-    c = _Call("moe_act_unpack8")
-    return c.run(stream, c.ptr(codes, "codes", _types(MOE_Q8), T * H),
-                 c.ptr(scales, "scales", _types("u8"), T * (H // 32)), T, H, c.ptr(x, "x", _types(x_dtype), T * H),
-                 x_dtype)
+    f = (_lib or _load()).moe_act_unpack8
+    n = "moe_act_unpack8"
+    d, codes = _p(None, n, "codes", codes, _T[MOE_Q8], T * H)
+    d, scales = _p(d, n, "scales", scales, _T["u8"], T * (H // 32))
+    d, x = _p(d, n, "x", x, _any(x_dtype), T * H)
+    return _run(f, d, stream, codes, scales, T, H, x, x_dtype)
 
 
 def moe_balance_ws_size(T, E):
-    from . import lib
-    return lib().moe_balance_ws_size(T, E)
+    return (_lib or _load()).moe_balance_ws_size(T, E)
 
 
 def moe_balance_loss(logits, topk_ids, token_mask, T, E, k, balance_coef, z_coef, counts, loss, ws=None, ws_bytes=0,
                      stream=None):
-    c = _Call("moe_balance_loss")
-    return c.run(stream, c.ptr(logits, "logits", _types(0), T * E), c.ptr(topk_ids, "topk_ids", _types("i32"), T * k),
-                 c.ptr(token_mask, "token_mask", _types("mask"), T), T, E, k, balance_coef, z_coef,
-                 c.ptr(counts, "counts", _types("i32"), E + 1), c.ptr(loss, "loss", _types(0), 4),
-                 c.ptr(ws, "ws", _types("u8"), ws_bytes), ws_bytes)
+    f = (_lib or _load()).moe_balance_loss
+    n = "moe_balance_loss"
+    d, logits = _p(None, n, "logits", logits, _T[0], T * E)
+    d, topk_ids = _p(d, n, "topk_ids", topk_ids, _T["i32"], T * k)
+    d, token_mask = _p(d, n, "token_mask", token_mask, _T["mask"], T)
+    d, counts = _p(d, n, "counts", counts, _T["i32"], E + 1)
+    d, loss = _p(d, n, "loss", loss, _T[0], 4)
+    d, ws = _p(d, n, "ws", ws, _T["u8"], ws_bytes)
+    return _run(f, d, stream, logits, topk_ids, token_mask, T, E, k, balance_coef, z_coef, counts, loss, ws, ws_bytes)
 
 
 def moe_route_backward(logits, topk_ids, topk_w, d_topk_w, token_mask, counts, d_loss, T, E, k, balance_coef, z_coef,
                        d_logits, dl_dtype, stream=None):
-    c = _Call("moe_route_backward")
-    return c.run(stream, c.ptr(logits, "logits", _types(0), T * E), c.ptr(topk_ids, "topk_ids", _types("i32"), T * k),
-                 c.ptr(topk_w, "topk_w", _types(0), T * k), c.ptr(d_topk_w, "d_topk_w", _types(0), T * k),
-                 c.ptr(token_mask, "token_mask", _types("mask"), T), c.ptr(counts, "counts", _types("i32"), E + 1),
-                 c.ptr(d_loss, "d_loss", _types(0), 1), T, E, k, balance_coef, z_coef,
-                 c.ptr(d_logits, "d_logits", _types(dl_dtype), T * E), dl_dtype)
+    f = (_lib or _load()).moe_route_backward
+    n = "moe_route_backward"
+    d, logits = _p(None, n, "logits", logits, _T[0], T * E)
+    d, topk_ids = _p(d, n, "topk_ids", topk_ids, _T["i32"], T * k)
+    d, topk_w = _p(d, n, "topk_w", topk_w, _T[0], T * k)
+    d, d_topk_w = _p(d, n, "d_topk_w", d_topk_w, _T[0], T * k)
+    d, token_mask = _p(d, n, "token_mask", token_mask, _T["mask"], T)
+    d, counts = _p(d, n, "counts", counts, _T["i32"], E + 1)
+    d, d_loss = _p(d, n, "d_loss", d_loss, _T[0], 1)
+    d, d_logits = _p(d, n, "d_logits", d_logits, _any(dl_dtype), T * E)
+    return _run(f, d, stream, logits, topk_ids, topk_w, d_topk_w, token_mask, counts, d_loss, T, E, k, balance_coef,
+                z_coef, d_logits, dl_dtype)
 
 
 def moe_expert_ffn_backward_ws_size(bits, T, k, H, I, E, mode=0):
-    from . import lib
-    return lib().moe_expert_ffn_backward_ws_size(bits, T, k, H, I, E, mode)
+    return (_lib or _load()).moe_expert_ffn_backward_ws_size(bits, T, k, H, I, E, mode)
 
 
 def moe_expert_ffn_backward(bits, expert_blobs, expert_offsets, active, perm_src, perm_dst, topk_w, x, x_dtype,
                             x_scales, dy, dy_dtype, T, k, H, I, E, shared_blob, dx, dx_dtype, d_topk_w, mode=0,
                             ws=None, ws_bytes=0, stream=None):
-    c = _Call("moe_expert_ffn_backward")
-    i32 = _types("i32")
-    blob = 3 * H * I * bits // 8 + 3 * H * I // 16
-    return c.run(stream, bits, c.ptr(expert_blobs, "expert_blobs", _types("i64"), E),
-                 c.ptr(expert_offsets, "expert_offsets", i32, E + 1), c.ptr(active, "active", i32, 1),
-                 c.ptr(perm_src, "perm_src", i32, T * k), c.ptr(perm_dst, "perm_dst", i32, T * k),
-                 c.ptr(topk_w, "topk_w", _types(0), T * k), c.ptr(x, "x", _types(x_dtype), T * H), x_dtype,
-                 c.ptr(x_scales, "x_scales", _types("u8"), T * (H // 32)), c.ptr(dy, "dy", _types(dy_dtype), T * H),
-                 dy_dtype, T, k, H, I, E, c.ptr(shared_blob, "shared_blob", _types("u8"), blob),
-                 c.ptr(dx, "dx", _types(dx_dtype), T * H), dx_dtype, c.ptr(d_topk_w, "d_topk_w", _types(0), T * k), mode,
-                 c.ptr(ws, "ws", _types("u8"), ws_bytes), ws_bytes)
+    f = (_lib or _load()).moe_expert_ffn_backward
+    n, i32 = "moe_expert_ffn_backward", _T["i32"]
+    d, expert_blobs = _p(None, n, "expert_blobs", expert_blobs, _T["i64"], E)
+    d, expert_offsets = _p(d, n, "expert_offsets", expert_offsets, i32, E + 1)
+    d, active = _p(d, n, "active", active, i32, 1)
+    d, perm_src = _p(d, n, "perm_src", perm_src, i32, T * k)
+    d, perm_dst = _p(d, n, "perm_dst", perm_dst, i32, T * k)
+    d, topk_w = _p(d, n, "topk_w", topk_w, _T[0], T * k)
+    d, x = _p(d, n, "x", x, _any(x_dtype), T * H)
+    d, x_scales = _p(d, n, "x_scales", x_scales, _T["u8"], T * (H // 32))
+    d, dy = _p(d, n, "dy", dy, _any(dy_dtype), T * H)
+    d, shared_blob = _p(d, n, "shared_blob", shared_blob, _T["u8"], 3 * H * I * bits // 8 + 3 * H * I // 16)
+    d, dx = _p(d, n, "dx", dx, _any(dx_dtype), T * H)
+    d, d_topk_w = _p(d, n, "d_topk_w", d_topk_w, _T[0], T * k)
+    d, ws = _p(d, n, "ws", ws, _T["u8"], ws_bytes)
+    return _run(f, d, stream, bits, expert_blobs, expert_offsets, active, perm_src, perm_dst, topk_w, x, x_dtype,
+                x_scales, dy, dy_dtype, T, k, H, I, E, shared_blob, dx, dx_dtype, d_topk_w, mode, ws, ws_bytes)
 
 
 def moe_router_backward_ws_size(T, H, E, dl_dtype, x_dtype, w_dtype):
-    from . import lib
-    return lib().moe_router_backward_ws_size(T, H, E, dl_dtype, x_dtype, w_dtype)
+    return (_lib or _load()).moe_router_backward_ws_size(T, H, E, dl_dtype, x_dtype, w_dtype)
 
 
 def moe_router_backward(d_logits, dl_dtype, x, x_dtype, w_router, w_dtype, dx_in, T, H, E, dx, dx_dtype, d_w, d_bias,
                         ws=None, ws_bytes=0, stream=None):
-    c = _Call("moe_router_backward")
-    return c.run(stream, c.ptr(d_logits, "d_logits", _types(dl_dtype), T * E), dl_dtype,
-                 c.ptr(x, "x", _types(x_dtype), T * H), x_dtype, c.ptr(w_router, "w_router", _types(w_dtype), E * H),
-                 w_dtype, c.ptr(dx_in, "dx_in", _types(0), T * H), T, H, E, c.ptr(dx, "dx", _types(dx_dtype), T * H),
-                 dx_dtype, c.ptr(d_w, "d_w", _types(w_dtype), E * H), c.ptr(d_bias, "d_bias", _types(0), E),
-                 c.ptr(ws, "ws", _types("u8"), ws_bytes), ws_bytes)
+    f = (_lib or _load()).moe_router_backward
+    n = "moe_router_backward"
+    d, d_logits = _p(None, n, "d_logits", d_logits, _any(dl_dtype), T * E)
+    d, x = _p(d, n, "x", x, _any(x_dtype), T * H)
+    d, w_router = _p(d, n, "w_router", w_router, _any(w_dtype), E * H)
+    d, dx_in = _p(d, n, "dx_in", dx_in, _T[0], T * H)
+    d, dx = _p(d, n, "dx", dx, _any(dx_dtype), T * H)
+    d, d_w = _p(d, n, "d_w", d_w, _any(w_dtype), E * H)
+    d, d_bias = _p(d, n, "d_bias", d_bias, _T[0], E)
+    d, ws = _p(d, n, "ws", ws, _T["u8"], ws_bytes)
+    return _run(f, d, stream, d_logits, dl_dtype, x, x_dtype, w_router, w_dtype, dx_in, T, H, E, dx, dx_dtype, d_w,
+                d_bias, ws, ws_bytes)
 
 
 class TrainStep:
