@@ -110,7 +110,7 @@ int moe_route_backward(const float *logits, const int32_t *topk_ids, const float
  *           own (undone in fp32 at the end), so that neither's scale matters;
  *           the gradients of g and u are rounded to fp16 between the two
  *           products.  fp32 accumulation.  Blobs in device memory.
- *           MOE_MODE_AUTO: GEMV up to 16 tokens, else GEMM.
+ *           MOE_MODE_AUTO: GEMV up to 6 tokens, else GEMM.
  *  Shapes as for moe_expert_ffn_*: H a multiple of 128 up to 8192, I up to 4096.
  *  ws: at least moe_expert_ffn_backward_ws_size(...) bytes. */
 size_t moe_expert_ffn_backward_ws_size(int bits, int T, int k, int H, int I, int E, int mode);

@@ -25,10 +25,12 @@ namespace moe {
 namespace {
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kBigThreads = 512;
+constexpr int kBigThreads = 1024;
 constexpr int kOneThreads = 1024;                 // the one-block form
 constexpr int kOneRows = 128;
 constexpr int kCountThreads = 1024;
+constexpr int kSlice = 4096;                      // experts a block counts, above 1024
+constexpr int kParts = 8;                         // blocks that count at most, up to 1024
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -131,38 +133,70 @@ __device__ __forceinline__ void finish_loss(double2 mine, double2 *part, unsigne
     }
 }
 
-// Counts this block's share of the (token, slot) pairs into hist [E + 1] (in
-// shared memory, zeroed), the last entry the tokens.
-__device__ __forceinline__ void count_pairs(const int32_t *ids, const uint8_t *mask, int T, int E, int k, int part,
-                                            int parts, int32_t *hist, unsigned *err) {
+// Counts (token, slot) pairs first, first + step, .. of the experts e0 .. e1 - 1
+// into hist (shared memory, zeroed: expert e at e - e0); returns the tokens met
+// at their first slot, added over the warp.  Four pairs' loads are in flight.
+__device__ __forceinline__ int count_pairs(const int32_t *ids, const uint8_t *mask, int T, int E, int k, int first,
+                                           int step, int e0, int e1, int32_t *hist, unsigned *err) {
     const int n = T * k;
     int tokens = 0;
-    for (int i = part * blockDim.x + threadIdx.x; i < n; i += parts * blockDim.x) {
-        const int t = i / k;
-        if (mask && !mask[t]) continue;
-        tokens += i == t * k;
-        const int e = ids[i];
-        if (e < 0 || e >= E) report(err, MOE_DEVERR_BAD_EXPERT);
-        else atomicAdd(hist + e, 1);
+    for (int i0 = first; i0 < n; i0 += 4 * step) {
+        int id[4], on[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const long i = i0 + static_cast<long>(u) * step;
+            const bool in = i < n;
+            const int t = in ? static_cast<int>(i) / k : 0;
+            id[u] = in ? ids[i] : 0;
+            on[u] = in && (!mask || mask[t]);
+            tokens += on[u] && i == static_cast<long>(t) * k;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (!on[u]) continue;
+            if (id[u] < 0 || id[u] >= E) report(err, MOE_DEVERR_BAD_EXPERT);
+            else if (id[u] >= e0 && id[u] < e1) atomicAdd(hist + id[u] - e0, 1);
+        }
     }
-    tokens = __reduce_add_sync(0xffffffffu, tokens);
-    if ((threadIdx.x & 31) == 0 && tokens) atomicAdd(hist + E, tokens);
+    return __reduce_add_sync(0xffffffffu, tokens);
 }
 }  // namespace
 
-// counts [parts, E + 1]: each block's part (one block: the counts themselves).
-__global__ void __launch_bounds__(kCountThreads) k_balance_counts(const int32_t *__restrict__ ids,
-                                                                  const uint8_t *__restrict__ mask, int T, int E, int k,
-                                                                  int32_t *__restrict__ counts, unsigned *ticket,
-                                                                  unsigned *err) {
-    extern __shared__ int32_t hist[];
+// Up to 1024 experts: each block counts its share of the pairs, out [blocks, E + 1].
+__global__ void __launch_bounds__(kCountThreads) k_balance_parts(const int32_t *__restrict__ ids,
+                                                                 const uint8_t *__restrict__ mask, int T, int E, int k,
+                                                                 int32_t *__restrict__ out, unsigned *ticket,
+                                                                 unsigned *err) {
+    __shared__ int32_t hist[1024 + 1];
     for (int e = threadIdx.x; e <= E; e += kCountThreads) hist[e] = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
     __syncthreads();
-    count_pairs(ids, mask, T, E, k, blockIdx.x, gridDim.x, hist, err);
+    const int tokens = count_pairs(ids, mask, T, E, k, blockIdx.x * kCountThreads + threadIdx.x,
+                                   gridDim.x * kCountThreads, 0, E, hist, err);
+    if ((threadIdx.x & 31) == 0 && tokens) atomicAdd(hist + E, tokens);
     __syncthreads();
-    int32_t *out = counts + static_cast<size_t>(blockIdx.x) * (E + 1);
-    for (int e = threadIdx.x; e <= E; e += kCountThreads) out[e] = hist[e];
+    for (int e = threadIdx.x; e <= E; e += kCountThreads) out[static_cast<size_t>(blockIdx.x) * (E + 1) + e] = hist[e];
+}
+
+// More experts: each block reads all pairs and counts kSlice experts.
+__global__ void __launch_bounds__(kCountThreads) k_balance_slices(const int32_t *__restrict__ ids,
+                                                                  const uint8_t *__restrict__ mask, int T, int E, int k,
+                                                                  int32_t *__restrict__ counts, unsigned *ticket,
+                                                                  unsigned *err) {
+    __shared__ int32_t hist[kSlice];
+    __shared__ int32_t all;
+    const int e0 = blockIdx.x * kSlice, e1 = min(E, e0 + kSlice);
+    for (int e = threadIdx.x; e < kSlice; e += kCountThreads) hist[e] = 0;
+    if (threadIdx.x == 0) {
+        all = 0;
+        if (blockIdx.x == 0) *ticket = 0;
+    }
+    __syncthreads();
+    const int tokens = count_pairs(ids, mask, T, E, k, threadIdx.x, kCountThreads, e0, e1, hist, err);
+    if ((threadIdx.x & 31) == 0 && tokens) atomicAdd(&all, tokens);
+    __syncthreads();
+    for (int e = e0 + threadIdx.x; e < e1; e += kCountThreads) counts[e] = hist[e - e0];
+    if (blockIdx.x == 0 && threadIdx.x == 0) counts[E] = all;
 }
 
 // Four neighbouring entries of a row from column c on (fill beyond E).
@@ -240,7 +274,8 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_rows(const float *__res
     __shared__ __align__(16) int32_t n[1024 + 4];
     for (int e = threadIdx.x; e <= E; e += kBalThreads) {
         int c = 0;
-        for (int p = 0; p < n_parts; ++p) c += parts[static_cast<size_t>(p) * (E + 1) + e];
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) c += p < n_parts ? parts[static_cast<size_t>(p) * (E + 1) + e] : 0;
         n[e] = c;
         if (blockIdx.x == 0) counts[e] = c;
     }
@@ -260,7 +295,8 @@ __global__ void __launch_bounds__(kOneThreads) k_balance_one(const float *__rest
     __shared__ __align__(16) int32_t n[1024 + 4];
     for (int e = threadIdx.x; e <= E; e += kOneThreads) n[e] = 0;
     __syncthreads();
-    count_pairs(ids, mask, T, E, k, 0, 1, n, err);
+    const int tokens = count_pairs(ids, mask, T, E, k, threadIdx.x, kOneThreads, 0, E, n, err);
+    if ((threadIdx.x & 31) == 0 && tokens) atomicAdd(n + E, tokens);
     __syncthreads();
     for (int e = threadIdx.x; e <= E; e += kOneThreads) counts[e] = n[e];
     const float unit = 1.f / (static_cast<float>(max(n[E], 1)) * k);
@@ -269,10 +305,10 @@ __global__ void __launch_bounds__(kOneThreads) k_balance_one(const float *__rest
     if (threadIdx.x == 0) write_loss(o, sum, n[E]);
 }
 
-// The sums of one row by a block, V float4 per thread (E <= 2048 V); on every thread.
+// The sums of one row by a block, V float4 per thread (E <= 4096 V); on every thread.
 template <int V, bool VEC>
-__device__ __forceinline__ Soft block_row(const float *row, int E, const int32_t *counts, float unit, float (&l)[V][4],
-                                          float (&f)[V][4]) {
+__device__ __forceinline__ Soft block_row(const float *row, int E, const int32_t *counts, float unit,
+                                          float (&l)[V][4]) {
     __shared__ float red[3][kBigThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -287,8 +323,9 @@ __device__ __forceinline__ Soft block_row(const float *row, int E, const int32_t
     a.m = warp_max(lane < kBigThreads / 32 ? red[0][lane] : -INFINITY);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        share4<VEC>(counts, 4 * (threadIdx.x + kBigThreads * i), E, unit, f[i]);
-        soft_exps(l[i], f[i], a.m, a.s, a.d);
+        float f[4];
+        share4<VEC>(counts, 4 * (threadIdx.x + kBigThreads * i), E, unit, f);
+        soft_exps(l[i], f, a.m, a.s, a.d);
     }
     a.s = warp_sum(a.s);
     a.d = warp_sum(a.d);
@@ -309,8 +346,8 @@ __global__ void __launch_bounds__(kBigThreads) k_balance_rows_big(const float *_
     RowSums sum = {0.f, 0.};
     for (int t = blockIdx.x; t < T; t += gridDim.x) {
         if (mask && !mask[t]) continue;
-        float l[V][4], f[V][4];
-        const RowSums r = row_sums(block_row<V, VEC>(logits + static_cast<size_t>(t) * E, E, counts, unit, l, f), err,
+        float l[V][4];
+        const RowSums r = row_sums(block_row<V, VEC>(logits + static_cast<size_t>(t) * E, E, counts, unit, l), err,
                                    threadIdx.x == 0);
         sum.d += r.d;
         sum.z += r.z;
@@ -458,12 +495,14 @@ __global__ void __launch_bounds__(kBigThreads) k_route_backward_big(RouteGrad a)
         RowGrad r = {0.f, 0.f, 0.f, 0.f};
         float v[V][4] = {};
         if (LOSS && on) {
-            float f[V][4];
-            r = row_grad(block_row<V, VEC>(a.logits + row, a.E, a.counts, unit, v, f), gb, gc, a.err, threadIdx.x == 0);
+            r = row_grad(block_row<V, VEC>(a.logits + row, a.E, a.counts, unit, v), gb, gc, a.err, threadIdx.x == 0);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < V; ++i) {
+                float f[4];                        // again, from L1
+                share4<VEC>(a.counts, 4 * (threadIdx.x + kBigThreads * i), a.E, unit, f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[i][j] = loss_term(r, v[i][j], f[i][j]);
+                for (int j = 0; j < 4; ++j) v[i][j] = loss_term(r, v[i][j], f[j]);
+            }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) put4<BF16, VEC>(a.dl, row, 4 * (threadIdx.x + kBigThreads * i), a.E, v[i]);
@@ -474,19 +513,18 @@ __global__ void __launch_bounds__(kBigThreads) k_route_backward_big(RouteGrad a)
 
 // ------------------------------------------------------------------ launch
 static int row_blocks(int T) {
-    const long want = (static_cast<long>(T) + kBalWarps - 1) / kBalWarps, cap = num_sms() * 8L;
+    // (measured at 8192 x 512: 4 blocks an SM, two rows a warp, against 8)
+    const long want = (static_cast<long>(T) + kBalWarps - 1) / kBalWarps, cap = num_sms() * 4L;
     return static_cast<int>(want < cap ? want : cap);
 }
 static int big_blocks(int T) {
-    const int cap = num_sms() * 2;
+    const int cap = num_sms();
     return T < cap ? T : cap;
 }
-// Blocks that count: up to eight while their parts are few numbers to add (up
-// to 1024 experts), each with at least 4096 pairs.
-static int count_parts(int T, int E, int k) {
-    if (E > 1024) return 1;
+// Blocks that count, up to 1024 experts: each with at least 4096 pairs.
+static int count_parts(int T, int k) {
     const long n = (static_cast<long>(T) * k + 4095) / 4096;
-    return static_cast<int>(n < 1 ? 1 : n < 8 ? n : 8);
+    return static_cast<int>(n < 1 ? 1 : n < kParts ? n : kParts);
 }
 
 struct BalanceWs {
@@ -504,7 +542,7 @@ static size_t carve(int T, int E, uint8_t *base, BalanceWs *out) {
     BalanceWs w;
     w.ticket = reinterpret_cast<unsigned *>(take(sizeof(unsigned)));
     w.part = reinterpret_cast<double2 *>(take((E <= 1024 ? row_blocks(T) : big_blocks(T)) * sizeof(double2)));
-    w.counts = reinterpret_cast<int32_t *>(take(E <= 1024 ? 8 * (static_cast<size_t>(E) + 1) * 4 : 0));
+    w.counts = reinterpret_cast<int32_t *>(take(E <= 1024 ? kParts * (static_cast<size_t>(E) + 1) * 4 : 0));
     if (out) *out = w;
     return at;
 }
@@ -531,9 +569,8 @@ static void by_big_row(int E, F &&go) {
         if (E % 4 == 0) go(nv, std::true_type{});
         else go(nv, std::false_type{});
     };
-    if (E <= 2048 * 4) v(integral_constant<int, 4>{});
-    else if (E <= 2048 * 8) v(integral_constant<int, 8>{});
-    else v(integral_constant<int, 16>{});
+    if (E <= 4096 * 2) v(integral_constant<int, 2>{});
+    else v(integral_constant<int, 8>{});
 }
 
 int launch_balance_loss(const float *logits, const int32_t *ids, const uint8_t *mask, int T, int E, int k,
@@ -550,13 +587,9 @@ int launch_balance_loss(const float *logits, const int32_t *ids, const uint8_t *
         count_launches(1);
         return cuda_status(cudaGetLastError(), "balance loss launch");
     }
-    const int parts = count_parts(T, E, k);
-    const size_t smem = (static_cast<size_t>(E) + 1) * sizeof(int32_t);
-    int rc = cuda_status(cudaFuncSetAttribute(k_balance_counts, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              static_cast<int>(smem)),
-                         "balance smem attribute");
-    if (rc) return rc;
-    k_balance_counts<<<parts, kCountThreads, smem, s>>>(ids, mask, T, E, k, E <= 1024 ? w.counts : counts, w.ticket, err);
+    const int parts = E <= 1024 ? count_parts(T, k) : 1;
+    if (E <= 1024) k_balance_parts<<<parts, kCountThreads, 0, s>>>(ids, mask, T, E, k, w.counts, w.ticket, err);
+    else k_balance_slices<<<(E + kSlice - 1) / kSlice, kCountThreads, 0, s>>>(ids, mask, T, E, k, counts, w.ticket, err);
     if (E <= 1024)
         by_row(E, [&](auto nv, auto vec) {
             k_balance_rows<decltype(nv)::value, decltype(vec)::value><<<row_blocks(T), kBalThreads, 0, s>>>(

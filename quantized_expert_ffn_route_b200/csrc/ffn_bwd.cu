@@ -1,16 +1,21 @@
 // Backward pass of the quantized experts on CUDA cores, fp32 throughout
 // (MOE_MODE_GEMV): a few tokens, where reading the weights is the cost.
 //
-// Three passes over an expert's weights' codes, for up to kNT rows at a time:
+// Three passes over an expert's weights' codes, for one or two rows at a time:
 //   1. g = Wg x, u = Wu x                       (dot products along a row)
 //   2. q = Wd^T dy, then dg, du and the strip's share of <q, h>   (columns)
 //   3. dxp = Wg^T dg + Wu^T du                                    (columns)
 // and a gather of each token's rows, weighted by its gates.  Passes 2 and 3
-// read a row's codes as they lie, four neighbouring blocks a row and eight
-// rows a warp (64-byte pieces at 4 bits), each lane keeping the 32 sums of its
-// block's columns in registers; lanes and warps are joined once at the end.
-// A weight is decoded exactly (code minus offset is a small whole number) and
-// once for all rows in flight.
+// read a row's codes as they lie, two (pass 2) or four neighbouring blocks a
+// row, each lane keeping the 32 sums of its block's columns in registers;
+// lanes and warps are joined once at the end.  A weight is decoded exactly
+// (code minus offset is a small whole number) and once for the rows in flight.
+//
+// At one token the passes are chains of memory latencies: four loads a lane
+// are in flight in passes 2 and 3, and pass 2, which has the fewest columns and
+// the longest sums, runs in strips of 64 columns and blocks of 16 warps.  The
+// shared expert's rows come first and split over tasks: left to one task each,
+// they were the tail at 16 tokens (187 us of pass 3).
 #include "common.cuh"
 #include "qdot.cuh"
 #include "train/ffn_bwd.cuh"
@@ -19,13 +24,17 @@ namespace moe {
 
 namespace {
 constexpr int kBwThreads = 256;
-constexpr int kBwWarps = kBwThreads / 32;
 constexpr int kNT = 2;             // rows in flight
-constexpr int kStrip = 128;        // columns of a pass 2 or 3 task: four blocks
+constexpr int kLoads = 4;          // weight rows a lane has in flight in passes 2 and 3
+// Passes 2 and 3: columns of a task and warps of a block.
+template <bool DOWN> struct Strip {
+    static constexpr int COLS = DOWN ? 64 : 128, BLOCKS = COLS / 32, WARPS = DOWN ? 16 : 8, THREADS = 32 * WARPS;
+    static constexpr int SUBS = 32 / BLOCKS;       // weight rows a warp reads at once
+};
 
 struct GemvBwdWs {
     float *gu;      // [T*k + T, 2I]: g, u, then dg, du
-    float *dwp;     // [T*k, I / kStrip]: shares of <q, h>
+    float *dwp;     // [T*k, I / 64]: shares of <q, h>
     float *dxp;     // [T*k + T, H]
     uint8_t *ok;    // [T*k]: the row's expert was computed
 };
@@ -47,6 +56,21 @@ __device__ __forceinline__ uint32_t block_piece(const uint32_t *w, int p) {
     if constexpr (BITS == 4) return (p < 4 ? w[p] : w[p - 4] >> 4) & 0x0F0F0F0Fu;
     else return (w[p & 1] >> (2 * (p >> 1))) & 0x03030303u;
 }
+
+// A task's group and rows.  The shared expert's tasks come first, kNT rows
+// each; a routed expert's take all its rows.
+struct Rows {
+    BwdGroup G;
+    int r0, r1;
+};
+__device__ __forceinline__ Rows task_rows(const FfnBackward &a, int item, int n_act, int chunks, bool say) {
+    if (item < chunks) {
+        BwdGroup G = {a.shared, a.T, -1};
+        return {G, item * kNT, min(a.T, (item + 1) * kNT)};
+    }
+    const BwdGroup G = bwd_group(a, item - chunks, n_act, say);
+    return {G, 0, G.n};
+}
 }  // namespace
 
 // Pass 1.  Task = (group, 16 weight rows): a warp takes two rows of both
@@ -57,19 +81,21 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_gateup(FfnBackward a, GemvBw
     extern __shared__ float4 xs[];                 // [kNT][piece][chunk]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), a.err);
-    const int n_groups = n_act + (a.shared ? 1 : 0), row_blocks = a.I / 16;
+    const int chunks = a.shared ? (a.T + kNT - 1) / kNT : 0;
+    const int n_items = n_act + chunks, row_blocks = a.I / 16;
     const int nch = a.H / Q::EPC, nsc = a.H / 32;
     const size_t rowb = static_cast<size_t>(a.H) * BITS / 8;
-    for (int task = blockIdx.x; task < n_groups * row_blocks; task += gridDim.x) {
-        const int g = task / row_blocks, rb = task - g * row_blocks;
-        const BwdGroup G = bwd_group(a, g, n_act, threadIdx.x == 0 && rb == 0);
+    for (long task = blockIdx.x; task < static_cast<long>(n_items) * row_blocks; task += gridDim.x) {
+        const int item = static_cast<int>(task / row_blocks), rb = static_cast<int>(task - static_cast<long>(item) * row_blocks);
+        const Rows R = task_rows(a, item, n_act, chunks, threadIdx.x == 0 && rb == 0);
+        const BwdGroup G = R.G;
         if (G.n <= 0) continue;
         const BlobView bv = blob_view(G.blob, BITS, a.H, a.I);
         const int i0 = rb * 16 + warp * 2;
         if (rb == 0 && G.row0 >= 0)
             for (int r = threadIdx.x; r < G.n; r += kBwThreads) ws.ok[G.row0 + r] = 1;
         const size_t out0 = G.row0 >= 0 ? G.row0 : static_cast<size_t>(a.T) * a.k;
-        for (int r0 = 0; r0 < G.n; r0 += kNT) {
+        for (int r0 = R.r0; r0 < R.r1; r0 += kNT) {
             __syncthreads();
             for (int t = 0; t < kNT; ++t) {
                 const bool in = r0 + t < G.n;
@@ -126,108 +152,133 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_gateup(FfnBackward a, GemvBw
     }
 }
 
+// The sums of NT rows of v (shared memory, M values each) over a warp's weight
+// rows, for the 32 columns of the lane's block.
+template <int BITS, bool DOWN, int NT>
+__device__ __forceinline__ void column_sums(const BlobView &bv, const float *vs, int M, int C, int I, int col0,
+                                            float (&acc)[kNT][32]) {
+    using S = Strip<DOWN>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane % S::BLOCKS, sub = lane / S::BLOCKS;
+    const size_t rowb = static_cast<size_t>(C) * BITS / 8;
+    const size_t cofs = static_cast<size_t>(col0 / 32 + blk) * 4 * BITS;
+    constexpr int STEP = S::SUBS * S::WARPS;
+    for (int m0 = S::SUBS * warp + sub; m0 < M; m0 += kLoads * STEP) {
+        uint32_t w[kLoads][BITS];
+        float d[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int m = m0 + u * STEP;
+            d[u] = 0.f;
+#pragma unroll
+            for (int x = 0; x < BITS; ++x) w[u][x] = 0;
+            if (m >= M) continue;
+            const uint8_t *codes = DOWN ? bv.cd : m < I ? bv.cg : bv.cu;
+            const __half *scl = DOWN ? bv.sd : m < I ? bv.sg : bv.su;
+            const size_t row = DOWN || m < I ? m : m - I;
+            if constexpr (BITS == 4) {
+                const uint4 c = __ldg(reinterpret_cast<const uint4 *>(codes + row * rowb + cofs));
+                w[u][0] = c.x, w[u][1] = c.y, w[u][2] = c.z, w[u][3] = c.w;
+            } else {
+                const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + row * rowb + cofs));
+                w[u][0] = c.x, w[u][1] = c.y;
+            }
+            d[u] = __half2float(scl[row * (C / 32) + col0 / 32 + blk]);
+        }
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int m = min(m0 + u * STEP, M - 1);           // beyond M: the step is zero
+            float vd[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) vd[t] = m0 + u * STEP < M ? d[u] * vs[t * M + m] : 0.f;
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                float q[4];
+                decode4<BITS>(block_piece<BITS>(w[u], p), q);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[t][4 * p + j] = fmaf(vd[t], q[j], acc[t][4 * p + j]);
+            }
+        }
+    }
+}
+
 // Passes 2 (DOWN: columns of Wd, along h) and 3 (columns of Wg, then Wu, along
-// i).  Task = (group, strip of 128 columns).
+// i).  Task = (rows, strip of columns).
 template <int BITS, bool DOWN>
-__global__ void __launch_bounds__(kBwThreads) k_bwd_columns(FfnBackward a, GemvBwdWs ws) {
+__global__ void __launch_bounds__(Strip<DOWN>::THREADS) k_bwd_columns(FfnBackward a, GemvBwdWs ws) {
+    using S = Strip<DOWN>;
     extern __shared__ float4 vmem[];
     const int M = DOWN ? a.H : 2 * a.I;            // rows summed over
     const int C = DOWN ? a.I : a.H;                // columns of the matrix
     float *vs = reinterpret_cast<float *>(vmem);   // [kNT][M]
-    float *red = vs + kNT * M;                     // [warp][kNT][kStrip]
-    __shared__ float wsum[kStrip * kNT / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane & 3, sub = lane >> 2;
+    float *red = vs + kNT * M;                     // [warp][kNT][COLS]
+    __shared__ float wsum[kNT * S::COLS / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane % S::BLOCKS, sub = lane / S::BLOCKS;
     const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), a.err);
-    const int n_groups = n_act + (a.shared ? 1 : 0), strips = C / kStrip;
-    const size_t rowb = static_cast<size_t>(C) * BITS / 8;
-    for (int task = blockIdx.x; task < n_groups * strips; task += gridDim.x) {
-        const int g = task / strips, st = task - g * strips;
-        const BwdGroup G = bwd_group(a, g, n_act, false);
+    const int chunks = a.shared ? (a.T + kNT - 1) / kNT : 0;
+    const int n_items = n_act + chunks, strips = C / S::COLS;
+    for (long task = blockIdx.x; task < static_cast<long>(n_items) * strips; task += gridDim.x) {
+        const int item = static_cast<int>(task / strips), st = static_cast<int>(task - static_cast<long>(item) * strips);
+        const Rows R = task_rows(a, item, n_act, chunks, false);
+        const BwdGroup G = R.G;
         if (G.n <= 0) continue;
         const BlobView bv = blob_view(G.blob, BITS, a.H, a.I);
         const size_t out0 = G.row0 >= 0 ? G.row0 : static_cast<size_t>(a.T) * a.k;
-        for (int r0 = 0; r0 < G.n; r0 += kNT) {
+        for (int r0 = R.r0; r0 < R.r1; r0 += kNT) {
+            const int nt = min(kNT, R.r1 - r0);
             __syncthreads();
-            for (int t = 0; t < kNT; ++t) {
-                const bool in = r0 + t < G.n;
-                const size_t tok = in && DOWN ? bwd_token(a, G, r0 + t) : 0;
-                for (int m4 = threadIdx.x; m4 < M / 4; m4 += kBwThreads) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (in)
-                        v = DOWN ? bwd_load4(a.dy, nullptr, a.dy_dtype, tok, a.H, m4)
-                                 : load4(ws.gu + (out0 + r0 + t) * 2 * a.I + 4 * m4);
-                    reinterpret_cast<float4 *>(vs + t * M)[m4] = v;
-                }
+            for (int t = 0; t < nt; ++t) {
+                const size_t tok = DOWN ? bwd_token(a, G, r0 + t) : 0;
+                for (int m4 = threadIdx.x; m4 < M / 4; m4 += S::THREADS)
+                    reinterpret_cast<float4 *>(vs + t * M)[m4] =
+                        DOWN ? bwd_load4(a.dy, nullptr, a.dy_dtype, tok, a.H, m4)
+                             : load4(ws.gu + (out0 + r0 + t) * 2 * a.I + 4 * m4);
             }
             __syncthreads();
             float acc[kNT][32] = {};
-#pragma unroll 2
-            for (int m = 8 * warp + sub; m < M; m += 8 * kBwWarps) {
-                const uint8_t *codes;
-                const __half *scl;
-                int row = m;
-                if (DOWN) codes = bv.cd, scl = bv.sd;
-                else if (m < a.I) codes = bv.cg, scl = bv.sg;
-                else codes = bv.cu, scl = bv.su, row = m - a.I;
-                const uint8_t *src = codes + row * rowb + (st * kStrip + 32 * blk) * BITS / 8;
-                uint32_t w[BITS];
-                if constexpr (BITS == 4) {
-                    const uint4 c = *reinterpret_cast<const uint4 *>(src);
-                    w[0] = c.x, w[1] = c.y, w[2] = c.z, w[3] = c.w;
-                } else {
-                    const uint2 c = *reinterpret_cast<const uint2 *>(src);
-                    w[0] = c.x, w[1] = c.y;
-                }
-                const float d = __half2float(scl[static_cast<size_t>(row) * (C / 32) + st * 4 + blk]);
-                float vd[kNT];
+            if (nt == 1) column_sums<BITS, DOWN, 1>(bv, vs, M, C, a.I, st * S::COLS, acc);
+            else column_sums<BITS, DOWN, kNT>(bv, vs, M, C, a.I, st * S::COLS, acc);
 #pragma unroll
-                for (int t = 0; t < kNT; ++t) vd[t] = d * vs[t * M + m];
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    float q[4];
-                    decode4<BITS>(block_piece<BITS>(w, p), q);
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[t][4 * p + j] = fmaf(vd[t], q[j], acc[t][4 * p + j]);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < kNT; ++t)
+            for (int t = 0; t < kNT; ++t) {
+                if (t >= nt) break;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     float v = acc[t][j];
-                    v += __shfl_xor_sync(0xffffffffu, v, 4);
-                    v += __shfl_xor_sync(0xffffffffu, v, 8);
-                    v += __shfl_xor_sync(0xffffffffu, v, 16);
-                    if (sub == (j & 7)) red[(warp * kNT + t) * kStrip + 32 * blk + j] = v;
-                }
-            __syncthreads();
-            // one thread per (row in flight, column): kNT * kStrip == kBwThreads
-            const int t = threadIdx.x / kStrip, c = threadIdx.x % kStrip;
-            float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kBwWarps; ++w) v += red[(w * kNT + t) * kStrip + c];
-            const bool in = r0 + t < G.n;
+                    for (int o = S::BLOCKS; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                    if (sub == j % S::SUBS) red[(warp * kNT + t) * S::COLS + 32 * blk + j] = v;
+                }
+            }
+            __syncthreads();
+            // one thread per (row in flight, column)
+            const int t = threadIdx.x / S::COLS, c = threadIdx.x % S::COLS;
+            const bool in = t < nt;
+            float v = 0.f;
+            if (in) {
+#pragma unroll
+                for (int w = 0; w < S::WARPS; ++w) v += red[(w * kNT + t) * S::COLS + c];
+            }
             if constexpr (DOWN) {
                 float share = 0.f;
                 if (in) {
-                    float *gu = ws.gu + (out0 + r0 + t) * 2 * a.I + st * kStrip + c;
+                    float *gu = ws.gu + (out0 + r0 + t) * 2 * a.I + st * S::COLS + c;
                     const float gv = gu[0], uv = gu[a.I], s = 1.f / (1.f + expf(-gv)), act = gv * s;
                     gu[0] = v * uv * fmaf(act, 1.f - s, s);
                     gu[a.I] = v * act;
                     share = v * act * uv;
                 }
                 share = warp_sum(share);
-                if (lane == 0) wsum[warp] = share;
+                if (lane == 0 && warp < kNT * S::COLS / 32) wsum[warp] = share;
                 __syncthreads();
                 if (c == 0 && in && G.row0 >= 0) {
                     float sum = 0.f;
-                    for (int w = 0; w < kStrip / 32; ++w) sum += wsum[t * (kStrip / 32) + w];
+#pragma unroll
+                    for (int w = 0; w < S::COLS / 32; ++w) sum += wsum[t * (S::COLS / 32) + w];
                     ws.dwp[(out0 + r0 + t) * strips + st] = sum;
                 }
             } else if (in) {
-                ws.dxp[(out0 + r0 + t) * a.H + st * kStrip + c] = v;
+                ws.dxp[(out0 + r0 + t) * a.H + st * S::COLS + c] = v;
             }
         }
     }
@@ -263,13 +314,22 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, const 
     __syncthreads();
     for (int h4 = threadIdx.x; h4 < a.H / 4; h4 += kBwThreads) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < a.k; ++i) {
-            if (row_s[i] < 0) continue;
-            const float4 v = load4(dxp + static_cast<size_t>(row_s[i]) * a.H + 4 * h4);
-            acc.x = fmaf(w_s[i], v.x, acc.x);
-            acc.y = fmaf(w_s[i], v.y, acc.y);
-            acc.z = fmaf(w_s[i], v.z, acc.z);
-            acc.w = fmaf(w_s[i], v.w, acc.w);
+        // eight slots' rows in flight, added in slot order
+        for (int i0 = 0; i0 < a.k; i0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[u] = i0 + u < a.k && row_s[i0 + u] >= 0 ? load4(dxp + static_cast<size_t>(row_s[i0 + u]) * a.H + 4 * h4)
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (i0 + u >= a.k || row_s[i0 + u] < 0) continue;
+                const float w = w_s[i0 + u];
+                acc.x = fmaf(w, v[u].x, acc.x);
+                acc.y = fmaf(w, v[u].y, acc.y);
+                acc.z = fmaf(w, v[u].z, acc.z);
+                acc.w = fmaf(w, v[u].w, acc.w);
+            }
         }
         if (a.shared) {
             const float4 v = load4(dxp + (static_cast<size_t>(a.T) * a.k + t) * a.H + 4 * h4);
@@ -301,7 +361,7 @@ static size_t carve(int T, int k, int H, int I, uint8_t *base, GemvBwdWs *out) {
     };
     GemvBwdWs w;
     w.gu = reinterpret_cast<float *>(take(all * 2 * I * 4));
-    w.dwp = reinterpret_cast<float *>(take(rows * (I / kStrip) * 4));
+    w.dwp = reinterpret_cast<float *>(take(rows * (I / Strip<true>::COLS) * 4));
     w.dxp = reinterpret_cast<float *>(take(all * H * 4));
     w.ok = take(rows);
     if (out) *out = w;
@@ -312,29 +372,28 @@ size_t ffn_backward_gemv_ws_bytes(int T, int k, int H, int I) { return carve(T, 
 
 template <int BITS>
 static int launch_gemv_bwd(const FfnBackward &a, const GemvBwdWs &w, cudaStream_t s) {
-    const long rows = static_cast<long>(a.T) * a.k, groups = (rows < a.E ? rows : a.E) + (a.shared ? 1 : 0);
+    const long rows = static_cast<long>(a.T) * a.k;
+    const long items = (rows < a.E ? rows : a.E) + (a.shared ? (a.T + kNT - 1) / kNT : 0);
     const long cap = num_sms() * 8L;
-    auto grid = [&](long per) { return groups * per < cap ? groups * per : cap; };
-    const int sm1 = kNT * a.H * 4;
-    auto columns = [&](int m) { return (kNT * m + kBwWarps * kNT * kStrip) * 4; };
-    int rc = cuda_status(cudaFuncSetAttribute(k_bwd_gateup<BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm1),
-                         "backward smem attribute");
+    auto grid = [&](long per) { return items * per < cap ? items * per : cap; };
+    using D = Strip<true>;
+    using U = Strip<false>;
+    const int sm1 = kNT * a.H * 4, sm2 = (kNT * a.H + D::WARPS * kNT * D::COLS) * 4;
+    const int sm3 = (kNT * 2 * a.I + U::WARPS * kNT * U::COLS) * 4;
+    auto smem = [](const void *f, int n) {
+        return cuda_status(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, n), "backward smem attribute");
+    };
+    int rc = smem(reinterpret_cast<const void *>(k_bwd_gateup<BITS>), sm1);
+    if (!rc) rc = smem(reinterpret_cast<const void *>(k_bwd_columns<BITS, true>), sm2);
+    if (!rc) rc = smem(reinterpret_cast<const void *>(k_bwd_columns<BITS, false>), sm3);
     if (rc) return rc;
     k_bwd_gateup<BITS><<<grid(a.I / 16), kBwThreads, sm1, s>>>(a, w);
-    rc = cuda_status(cudaFuncSetAttribute(k_bwd_columns<BITS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          columns(a.H)),
-                     "backward smem attribute");
-    if (rc) return rc;
-    k_bwd_columns<BITS, true><<<grid(a.I / kStrip), kBwThreads, columns(a.H), s>>>(a, w);
-    rc = cuda_status(cudaFuncSetAttribute(k_bwd_columns<BITS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          columns(2 * a.I)),
-                     "backward smem attribute");
-    if (rc) return rc;
-    k_bwd_columns<BITS, false><<<grid(a.H / kStrip), kBwThreads, columns(2 * a.I), s>>>(a, w);
+    k_bwd_columns<BITS, true><<<grid(a.I / D::COLS), D::THREADS, sm2, s>>>(a, w);
+    k_bwd_columns<BITS, false><<<grid(a.H / U::COLS), U::THREADS, sm3, s>>>(a, w);
     count_launches(3);
     rc = cuda_status(cudaGetLastError(), "expert backward launch");
     if (rc) return rc;
-    return launch_ffn_backward_gather(a, w.dxp, w.dwp, a.I / kStrip, w.ok, nullptr, s);
+    return launch_ffn_backward_gather(a, w.dxp, w.dwp, a.I / D::COLS, w.ok, nullptr, s);
 }
 
 int launch_ffn_backward_gather(const FfnBackward &a, const float *dxp, const float *dwp, int shares,

@@ -498,7 +498,7 @@ def test_train_step(wdt, T, mode):
     assert np.array_equal(step.counts.cpu().numpy(), counts)
     assert np.allclose(loss.cpu().numpy(), losses, rtol=1e-5)          # the call's own test has the bound
     xv = R.act8(x)[2]
-    gemm = not (mode == M.MOE_MODE_GEMV or T <= 16)
+    gemm = not (mode == M.MOE_MODE_GEMV or T <= 6)
     dx, dw, ex, ew = R.experts_backward(4, H, I, lay.blobs, lay.shared, ids, w, xv, dy.astype(np.float64),
                                         R.U16 if gemm else 0.0)
     want_dl = dl * lgrad + R.gates(ids, w, dw, E, mask != 0)
