@@ -27,7 +27,7 @@
 //       a thread between two barriers;
 //   loader warps fill the B stages: phase 1 gathers the tokens' rows with
 //       cp.async (TMA's four-row gathers took 50 cycles each here: 1842 us at
-//       8192 tokens), phase 2 one warp with TMA boxes of 64 K rows x 64 tokens;
+//       8192 tokens), phase 2 one warp with TMA boxes of 128 K rows x 64 tokens;
 //   one thread issues tcgen05.mma; four warps read the accumulators.
 // Every wait is bounded (MOE_DEVERR_TIMEOUT; all roles then leave their loops
 // and TMEM is freed).
@@ -363,18 +363,18 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         int sb = 0, issued = 0;
         uint32_t phase = 1;
         bool ok = true;
+        const uint32_t on = elect_one();
         if (lane == 0) tma_prefetch_map(&map);
         for (int i = 0; i < n_my && ok; ++i) {
             int m0;
             const TokTile te = tile_of(i, m0);
-            const int half = lane & 1, n0 = (lane >> 1) * 64, boxes = (te.n + 63) / 64;
+            const int n = __shfl_sync(0xffffffffu, te.n, 0), at = __shfl_sync(0xffffffffu, te.at, 0);
             for (int s = 0; s < nk; ++s) {
                 if (!(ok = wait(emptyB + sb, phase))) break;
                 const uint32_t dst = smem_addr(smem + C::OFF_B + sb * C::B_STAGE);
-                if (lane == 0) mbar_arrive_expect_tx(fullB + sb, 2 * boxes * 8192);
-                __syncwarp();
-                if (n0 < te.n)
-                    tma_load_2d(dst + half * C::B_TILE + n0 * 128, &map, te.at + n0, (2 * s + half) * kBK, fullB + sb);
+                expect_tx_on(on, fullB + sb, (n + 63) / 64 * 128 * 128);
+                for (int n0 = 0; n0 < n; n0 += 64)            // 128 K rows of 64 tokens
+                    tma_load_on(on, dst + n0 * 256, &map, at + n0, s * C::KSTAGE, fullB + sb);
                 if (++sb == SB) sb = 0, phase ^= 1;
                 ++issued;
             }
@@ -485,6 +485,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         const uint32_t on = elect_one();
         const uint32_t ring = smem_addr(smem), tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t mn = desc_mn_sw128(ring, 8192, 1024), km = desc_sw128(ring);
+        const uint64_t mnb = desc_mn_sw128(ring, 16384, 1024);          // phase 2's B: atoms of 128 K rows
         int sa = 0, sb = 0;
         uint32_t pa = 0, pb = 0;
         bool ok = true;
@@ -505,11 +506,11 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
                 for (int mat = 0; mat < NM; ++mat) {
                     const bool trans = PHASE == 2 || mat == 2;
                     const uint64_t am = as + mat * (kMat >> 4);
-                    const uint64_t bm = bs + (PHASE == 1 ? mat == 2 : mat) * (C::B_TILE >> 4);
+                    const uint64_t bm = bs + (PHASE == 1 ? (mat == 2) * (C::B_TILE >> 4) : mat * (8192 >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         mma_f16_on(on, d + (PHASE == 1 ? mat : 0) * MAXN, trans ? mn + am + kk * 128 : km + am + kk * 2,
-                                   PHASE == 2 ? mn + bm + kk * 128 : km + bm + kk * 2, trans ? id_mn : id_k, (PHASE == 1 ? s | kk : s | kk | mat) != 0);
+                                   PHASE == 2 ? mnb + bm + kk * 128 : km + bm + kk * 2, trans ? id_mn : id_k, (PHASE == 1 ? s | kk : s | kk | mat) != 0);
                 }
                 mma_commit_on(on, emptyA + sa);
                 mma_commit_on(on, emptyB + sb);
@@ -754,7 +755,7 @@ int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     TcArgs p2 = p;
     p2.tiles = w.tiles2, p2.n_tiles = w.counts + 1;
     CUtensorMap map;
-    rc = make_tensor_map(&map, w.gu16, 0, 2 * static_cast<uint64_t>(a.I), plan.cols, plan.cols * 2, kBK);
+    rc = make_tensor_map(&map, w.gu16, 0, 2 * static_cast<uint64_t>(a.I), plan.cols, plan.cols * 2, 2 * kBK);
     if (rc) return rc;
     if (a.bits == 4) {
         rc = plan.large ? launch_phase<4, 1, kLargeN1>(p, map, s) : launch_phase<4, 1, kSmallN>(p, map, s);

@@ -28,13 +28,14 @@ using namespace sm100;
 
 namespace {
 constexpr int kRM = 128, kRK = 64;
-constexpr int kRNx = 256, kRNw = 128;              // N of a tile of dx (tokens), dW (experts)
-constexpr int kRStages = 4;
+constexpr int kRN = 128;                           // N of a tile: tokens (dx), experts (dW)
+constexpr int kRStages = 6, kRAcc = 4;
 constexpr int kREpi = 8;
 constexpr int kRThreads = 32 * (2 + kREpi);
-constexpr uint32_t kRA = kRM * kRK * 2, kRStage = kRA + kRNx * kRK * 2;
+constexpr uint32_t kRA = kRM * kRK * 2, kRStage = kRA + kRN * kRK * 2;
 constexpr uint32_t kROffBar = kRStages * kRStage;
-constexpr uint32_t kRSmem = kROffBar + 16 * 8 + 16 + 1024;
+constexpr uint32_t kRSmem = kROffBar + 24 * 8 + 16 + 1024;
+static_assert(2 * kRStages + 2 * kRAcc + 1 <= 24 && kRAcc * kRN <= 512, "barriers and TMEM columns");
 constexpr long kRSpin = 1L << 22;
 constexpr int kBiasRows = 64;                      // rows of dl a block sums at least
 
@@ -64,14 +65,14 @@ __device__ __forceinline__ Unit unit_of(const RouterArgs &a, int u) {
     j.m0 = (v - r * a.mt) * kRM;
     if (j.w) {
         j.split = r / a.et;
-        j.n0 = (r - j.split * a.et) * kRNw;
-        j.N = min(kRNw, (a.E - j.n0 + 15) & ~15);
+        j.n0 = (r - j.split * a.et) * kRN;
+        j.N = min(kRN, (a.E - j.n0 + 15) & ~15);
         j.k0 = j.split * a.per_split;
         j.nk = min(a.per_split, (a.T + kRK - 1) / kRK - j.k0);
     } else {
         j.split = 0;
-        j.n0 = r * kRNx;
-        j.N = min(kRNx, (a.T - j.n0 + 15) & ~15);
+        j.n0 = r * kRN;
+        j.N = min(kRN, (a.T - j.n0 + 15) & ~15);
         j.k0 = 0;
         j.nk = (a.E + kRK - 1) / kRK;
     }
@@ -86,9 +87,9 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kROffBar);
-    uint64_t *full = bars, *empty = bars + kRStages, *accF = bars + 2 * kRStages, *accE = accF + 2, *drain = accF + 4;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 16);
-    volatile int &abort_s = *(reinterpret_cast<int *>(bars + 16) + 1);
+    uint64_t *full = bars, *empty = bars + kRStages, *accF = bars + 2 * kRStages, *accE = accF + kRAcc, *drain = accE + kRAcc;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 24);
+    volatile int &abort_s = *(reinterpret_cast<int *>(bars + 24) + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         abort_s = 0;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
             mbar_init(full + i, 1);
             mbar_init(empty + i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kRAcc; ++i) {
             mbar_init(accF + i, 1);
             mbar_init(accE + i, kREpi);
         }
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
 
     if (warp == 0) {
         // -------------------------------------------------------------- TMA
+        const uint32_t on = elect_one();
         int st = 0, issued = 0;
         uint32_t phase = 1;
         bool ok = true;
@@ -134,13 +136,18 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
                 if (!(ok = wait(empty + st, phase))) break;
                 const uint32_t sa = smem_addr(smem + st * kRStage), sb = sa + kRA;
                 const int k = (j.k0 + s) * kRK;
-                if (lane == 0) mbar_arrive_expect_tx(full + st, j.w ? kRA + kRNw * kRK * 2 : kRStage);
-                __syncwarp();
-                // two boxes of 64 h; dl: one box of 256 tokens, or two of 64 experts
-                if (lane < 2) tma_load_2d(sa + lane * 8192, j.w ? &map_x : &map_w, j.m0 + 64 * lane, k, full + st);
-                else if (j.w && lane < 4)
-                    tma_load_2d(sb + (lane - 2) * 8192, &map_dl_mn, j.n0 + 64 * (lane - 2), k, full + st);
-                else if (!j.w && lane == 2) tma_load_2d(sb, &map_dl_k, k, j.n0, full + st);
+                expect_tx_on(on, full + st, kRStage);
+                // two boxes of 64 h; dl: one box of 128 tokens, or two of 64 experts
+                if (j.w) {
+                    tma_load_on(on, sa, &map_x, j.m0, k, full + st);
+                    tma_load_on(on, sa + 8192, &map_x, j.m0 + 64, k, full + st);
+                    tma_load_on(on, sb, &map_dl_mn, j.n0, k, full + st);
+                    tma_load_on(on, sb + 8192, &map_dl_mn, j.n0 + 64, k, full + st);
+                } else {
+                    tma_load_on(on, sa, &map_w, j.m0, k, full + st);
+                    tma_load_on(on, sa + 8192, &map_w, j.m0 + 64, k, full + st);
+                    tma_load_on(on, sb, &map_dl_k, k, j.n0, full + st);
+                }
                 if (++st == kRStages) st = 0, phase ^= 1;
                 ++issued;
             }
@@ -158,8 +165,8 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
         bool ok = true;
         for (int u = bid; u < a.units && ok; u += grid, ++i) {
             const Unit j = unit_of(a, u);
-            const uint32_t idesc = idesc_16bit(1, 1, j.w, kRM, j.N), d = tm + (i & 1) * 256;
-            if (!(ok = wait(accE + (i & 1), ((i >> 1) & 1) ^ 1))) break;
+            const uint32_t idesc = idesc_16bit(1, 1, j.w, kRM, j.N), d = tm + (i % kRAcc) * kRN;
+            if (!(ok = wait(accE + i % kRAcc, ((i / kRAcc) & 1) ^ 1))) break;
             tc_fence_after();
             for (int s = 0; s < j.nk; ++s) {
                 if (!(ok = wait(full + st, phase))) break;
@@ -171,7 +178,7 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
                 mma_commit_on(on, empty + st);
                 if (++st == kRStages) st = 0, phase ^= 1;
             }
-            mma_commit_on(on, accF + (i & 1));
+            mma_commit_on(on, accF + i % kRAcc);
         }
         mma_commit_on(on, drain);
         bool done = false;
@@ -198,54 +205,67 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
                 out[e + 1] = s1;
             }
         }
+        // A warp has every second chunk of 16 columns of its lanes.  dx_in is what it waits for: a
+        // unit's values are asked for while the unit before is written, chunk by chunk.
+        constexpr int CH = kRN / 32;
+        const int half = ew >> 2;
+        float add[CH][16];
+        auto fetch = [&](const Unit &j, int c) {
+            const int c0 = 32 * c + 16 * half, ncol = a.T - j.n0 - c0, h = j.m0 + m;
+            const bool on = !j.w && a.dx_in && h < a.H;
+            const float *src = a.dx_in + static_cast<size_t>(j.n0 + c0) * a.H + h;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) add[c][e] = on && e < ncol ? src[static_cast<size_t>(e) * a.H] : 0.f;
+        };
+        Unit j = {};
+        if (bid < a.units) {
+            j = unit_of(a, bid);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) fetch(j, c);
+        }
         int i = 0;
         for (int u = bid; u < a.units; u += grid, ++i) {
-            const Unit j = unit_of(a, u);
-            const int h = j.m0 + m, half = ew >> 2;                   // chunks of 16 columns, alternately
+            const bool more = u + grid < a.units;
+            Unit next = j;
+            if (more) next = unit_of(a, u + grid);
+            const int h = j.m0 + m, ncol = j.w ? a.E - j.n0 : a.T - j.n0;     // columns that exist
             const bool in = h < a.H;
-            const int ncol = j.w ? a.E - j.n0 : a.T - j.n0;           // columns that exist
-            // dx_in of a chunk is on its way before the accumulators are, and
-            // the next chunk's while this one is written
-            float add[16];
-            auto fetch = [&](int c0) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    add[e] = !j.w && a.dx_in && in && c0 + e < ncol && c0 < j.N
-                                 ? a.dx_in[static_cast<size_t>(j.n0 + c0 + e) * a.H + h] : 0.f;
-            };
-            fetch(16 * half);
-            if (!wait(accF + (i & 1), (i >> 1) & 1)) break;
+            if (!wait(accF + i % kRAcc, (i / kRAcc) & 1)) break;
             tc_fence_after();
-            const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + (i & 1) * 256;
-            for (int c0 = 16 * half; c0 < j.N; c0 += 32) {
-                float v[16];
-                tmem_ld16(base + c0, v);
-                tmem_ld_wait();
+            const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + (i % kRAcc) * kRN;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] += add[e];
-                fetch(c0 + 32);
-                if (!in) continue;
-                if (j.w && a.splits > 1) {
-                    float *out = a.dw_part + (static_cast<size_t>(j.split) * a.E + j.n0 + c0) * a.H + h;
+            for (int c = 0; c < CH; ++c) {
+                const int c0 = 32 * c + 16 * half;
+                if (c0 < j.N) {
+                    float v[16];
+                    tmem_ld16(base + c0, v);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (c0 + e < ncol) out[static_cast<size_t>(e) * a.H] = v[e];
-                } else if (j.w || a.dx_bf16) {
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(j.w ? a.dw : a.dx) +
-                                         static_cast<size_t>(j.n0 + c0) * a.H + h;
+                    for (int e = 0; e < 16; ++e) v[e] += add[c][e];
+                    if (j.w && a.splits > 1) {
+                        float *out = a.dw_part + (static_cast<size_t>(j.split) * a.E + j.n0 + c0) * a.H + h;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (c0 + e < ncol) out[static_cast<size_t>(e) * a.H] = __float2bfloat16_rn(v[e]);
-                } else {
-                    float *out = static_cast<float *>(a.dx) + static_cast<size_t>(j.n0 + c0) * a.H + h;
+                        for (int e = 0; e < 16; ++e)
+                            if (in && c0 + e < ncol) out[static_cast<size_t>(e) * a.H] = v[e];
+                    } else if (j.w || a.dx_bf16) {
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(j.w ? a.dw : a.dx) +
+                                             static_cast<size_t>(j.n0 + c0) * a.H + h;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (c0 + e < ncol) out[static_cast<size_t>(e) * a.H] = v[e];
+                        for (int e = 0; e < 16; ++e)
+                            if (in && c0 + e < ncol) out[static_cast<size_t>(e) * a.H] = __float2bfloat16_rn(v[e]);
+                    } else {
+                        float *out = static_cast<float *>(a.dx) + static_cast<size_t>(j.n0 + c0) * a.H + h;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (in && c0 + e < ncol) out[static_cast<size_t>(e) * a.H] = v[e];
+                    }
                 }
+                if (more) fetch(next, c);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(accE + (i & 1));
+            if (lane == 0) mbar_arrive(accE + i % kRAcc);
+            j = next;
         }
     }
     tc_fence_before();
@@ -292,7 +312,7 @@ struct RouterPlan {
 RouterPlan router_plan(int T, int H, int E) {
     RouterPlan p;
     p.mt = (H + kRM - 1) / kRM;
-    p.et = (E + kRNw - 1) / kRNw;
+    p.et = (E + kRN - 1) / kRN;
     const int steps = (T + kRK - 1) / kRK;
     // as many splits as give every SM a unit, each of at least 8 k-steps (a
     // split costs E x H x 8 bytes of traffic)
@@ -332,7 +352,7 @@ int launch_router_backward_tc(const RouterBackward &b, void *ws, cudaStream_t s)
     a.mt = p.mt, a.et = p.et, a.splits = p.splits, a.per_split = p.per_split;
     a.bias_parts = p.bias_parts;
     a.units_w = b.d_w ? p.mt * p.et * p.splits : 0;
-    a.units = a.units_w + (b.dx ? p.mt * ((b.T + kRNx - 1) / kRNx) : 0);
+    a.units = a.units_w + (b.dx ? p.mt * ((b.T + kRN - 1) / kRN) : 0);
     a.err = b.err;
     const long hook = static_cast<long>(test_hook_value(MOE_HOOK_GEMM_SPIN));
     a.spin = hook > 0 ? hook : kRSpin;
@@ -340,7 +360,7 @@ int launch_router_backward_tc(const RouterBackward &b, void *ws, cudaStream_t s)
     CUtensorMap mw = {}, mx = {}, mk = {}, mm = {};
     int rc = MOE_OK;
     if (b.dx && ((rc = make_tensor_map(&mw, b.w, 1, b.E, b.H, hb, kRK)) ||
-                 (rc = make_tensor_map(&mk, b.dl, 1, b.T, b.E, eb, kRNx))))
+                 (rc = make_tensor_map(&mk, b.dl, 1, b.T, b.E, eb, kRN))))
         return rc;
     if (b.d_w && ((rc = make_tensor_map(&mx, b.x, 1, b.T, b.H, hb, kRK)) ||
                   (rc = make_tensor_map(&mm, b.dl, 1, b.T, b.E, eb, kRK))))

@@ -16,12 +16,23 @@ int make_tensor_map(CUtensorMap *map, const void *base, int bf16, uint64_t rows,
 
 namespace sm100 {
 
-// A box of the map at (column x, row y) to shared memory, counted on `bar`.  x
-// a multiple of 8 values.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+// A box of the map at (column x, row y) to shared memory, counted on `bar`, by
+// the lane whose `on` is 1 (the whole warp calls, with the same operands: the
+// instruction reads uniform registers, and operands that differ by lane make a
+// loop over the lanes of it).  x a multiple of 8 values.
+__device__ __forceinline__ void tma_load_on(uint32_t on, uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            uint64_t *bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        "{ .reg .pred q; setp.ne.b32 q, %5, 0; "
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4]; }"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar)), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void expect_tx_on(uint32_t on, uint64_t *bar, uint32_t bytes) {
+    asm volatile(
+        "{ .reg .pred q; .reg .b64 st; setp.ne.b32 q, %2, 0; "
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(smem_addr(bar)),
+        "r"(bytes), "r"(on)
         : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
