@@ -206,61 +206,65 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
             }
         }
         // A warp has every second chunk of 16 columns of its lanes.  dx_in is what it waits for: a
-        // unit's values are asked for while the unit before is written, chunk by chunk.
-        constexpr int CH = kRN / 32;
+        // unit's lines are brought to L2 a unit ahead, a chunk's values to registers a chunk ahead.
+        // (The loop stays rolled: unrolled with two units' values in registers it was slower, its code
+        // being read by eight warps.)
         const int half = ew >> 2;
-        float add[CH][16];
-        auto fetch = [&](const Unit &j, int c) {
-            const int c0 = 32 * c + 16 * half, ncol = a.T - j.n0 - c0, h = j.m0 + m;
-            const bool on = !j.w && a.dx_in && h < a.H;
-            const float *src = a.dx_in + static_cast<size_t>(j.n0 + c0) * a.H + h;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) add[c][e] = on && e < ncol ? src[static_cast<size_t>(e) * a.H] : 0.f;
+        auto prefetch = [&](const Unit &j) {
+            // 128 tokens x 512 bytes: the warp's 16 tokens, a line a lane and step
+            if (j.w || !a.dx_in) return;
+            for (int e = lane >> 2; e < 16; e += 8) {
+                const int t = j.n0 + 16 * ew + e, h = j.m0 + 32 * (lane & 3);
+                if (t < a.T && h < a.H)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dx_in + static_cast<size_t>(t) * a.H + h));
+            }
         };
         Unit j = {};
         if (bid < a.units) {
             j = unit_of(a, bid);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) fetch(j, c);
+            prefetch(j);
         }
         int i = 0;
         for (int u = bid; u < a.units; u += grid, ++i) {
-            const bool more = u + grid < a.units;
             Unit next = j;
-            if (more) next = unit_of(a, u + grid);
-            const int h = j.m0 + m, ncol = j.w ? a.E - j.n0 : a.T - j.n0;     // columns that exist
-            const bool in = h < a.H;
+            if (u + grid < a.units) {
+                next = unit_of(a, u + grid);
+                prefetch(next);
+            }
+            const int h = j.m0 + m, ncol = h < a.H ? (j.w ? a.E : a.T) - j.n0 : 0;      // columns to write
+            const bool add = !j.w && a.dx_in, wide = j.w ? a.splits > 1 : !a.dx_bf16;
+            const float *src = a.dx_in + static_cast<size_t>(j.n0) * a.H + h;
+            void *dst = j.w ? (wide ? static_cast<void *>(a.dw_part) : a.dw) : a.dx;
+            const size_t at = static_cast<size_t>((j.w && wide ? static_cast<size_t>(j.split) * a.E : 0) + j.n0) * a.H + h;
+            float in[16];
+            auto fetch = [&](int c0) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    in[e] = add && c0 + e < ncol ? src[static_cast<size_t>(c0 + e) * a.H] : 0.f;
+            };
+            fetch(16 * half);
             if (!wait(accF + i % kRAcc, (i / kRAcc) & 1)) break;
             tc_fence_after();
             const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + (i % kRAcc) * kRN;
+#pragma unroll 1
+            for (int c0 = 16 * half; c0 < j.N; c0 += 32) {
+                float v[16];
+                tmem_ld16(base + c0, v);
+                tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int c0 = 32 * c + 16 * half;
-                if (c0 < j.N) {
-                    float v[16];
-                    tmem_ld16(base + c0, v);
-                    tmem_ld_wait();
+                for (int e = 0; e < 16; ++e) v[e] += in[e];
+                fetch(c0 + 32);
+                const size_t o = at + static_cast<size_t>(c0) * a.H;
+                if (wide) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] += add[c][e];
-                    if (j.w && a.splits > 1) {
-                        float *out = a.dw_part + (static_cast<size_t>(j.split) * a.E + j.n0 + c0) * a.H + h;
+                    for (int e = 0; e < 16; ++e)
+                        if (c0 + e < ncol) static_cast<float *>(dst)[o + static_cast<size_t>(e) * a.H] = v[e];
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (in && c0 + e < ncol) out[static_cast<size_t>(e) * a.H] = v[e];
-                    } else if (j.w || a.dx_bf16) {
-                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(j.w ? a.dw : a.dx) +
-                                             static_cast<size_t>(j.n0 + c0) * a.H + h;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (in && c0 + e < ncol) out[static_cast<size_t>(e) * a.H] = __float2bfloat16_rn(v[e]);
-                    } else {
-                        float *out = static_cast<float *>(a.dx) + static_cast<size_t>(j.n0 + c0) * a.H + h;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (in && c0 + e < ncol) out[static_cast<size_t>(e) * a.H] = v[e];
-                    }
+                    for (int e = 0; e < 16; ++e)
+                        if (c0 + e < ncol)
+                            static_cast<__nv_bfloat16 *>(dst)[o + static_cast<size_t>(e) * a.H] = __float2bfloat16_rn(v[e]);
                 }
-                if (more) fetch(next, c);
             }
             tc_fence_before();
             __syncwarp();
