@@ -15,7 +15,7 @@
 // tokens, 512 experts and 2048 hidden the 64 tiles of dW alone would take 128
 // k-steps each on 64 SMs.
 //
-// Roles: warp 0 TMA, warp 1 MMA, warps 2-9 epilogue (they sum their block's
+// Roles: warp 0 TMA, warp 1 MMA, warps 2 on epilogue (they sum their block's
 // rows of dl for db before their first tile).  Waits are bounded.
 #include "common.cuh"
 #include "kernels.h"
@@ -30,7 +30,7 @@ namespace {
 constexpr int kRM = 128, kRK = 64;
 constexpr int kRN = 128;                           // N of a tile: tokens (dx), experts (dW)
 constexpr int kRStages = 6, kRAcc = 4;
-constexpr int kREpi = 8;
+constexpr int kREpi = 16;
 constexpr int kRThreads = 32 * (2 + kREpi);
 constexpr uint32_t kRA = kRM * kRK * 2, kRStage = kRA + kRN * kRK * 2;
 constexpr uint32_t kROffBar = kRStages * kRStage;
@@ -205,16 +205,16 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
                 out[e + 1] = s1;
             }
         }
-        // A warp has every second chunk of 16 columns of its lanes.  dx_in is what it waits for: a
+        // A warp has every (kREpi / 4)th chunk of 16 columns of its lanes.  dx_in is what it waits for: a
         // unit's lines are brought to L2 a unit ahead, a chunk's values to registers a chunk ahead.
         // (The loop stays rolled: unrolled with two units' values in registers it was slower, its code
         // being read by eight warps.)
-        const int half = ew >> 2;
+        const int part = ew >> 2;
         auto prefetch = [&](const Unit &j) {
-            // 128 tokens x 512 bytes: the warp's 16 tokens, a line a lane and step
+            // 128 tokens x 512 bytes: the warp's share of tokens, a line a lane
             if (j.w || !a.dx_in) return;
-            for (int e = lane >> 2; e < 16; e += 8) {
-                const int t = j.n0 + 16 * ew + e, h = j.m0 + 32 * (lane & 3);
+            for (int e = lane >> 2; e < kRN / kREpi; e += 8) {
+                const int t = j.n0 + kRN / kREpi * ew + e, h = j.m0 + 32 * (lane & 3);
                 if (t < a.T && h < a.H)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dx_in + static_cast<size_t>(t) * a.H + h));
             }
@@ -242,18 +242,18 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
                 for (int e = 0; e < 16; ++e)
                     in[e] = add && c0 + e < ncol ? src[static_cast<size_t>(c0 + e) * a.H] : 0.f;
             };
-            fetch(16 * half);
+            fetch(16 * part);
             if (!wait(accF + i % kRAcc, (i / kRAcc) & 1)) break;
             tc_fence_after();
             const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + (i % kRAcc) * kRN;
 #pragma unroll 1
-            for (int c0 = 16 * half; c0 < j.N; c0 += 32) {
+            for (int c0 = 16 * part; c0 < j.N; c0 += 4 * kREpi) {
                 float v[16];
                 tmem_ld16(base + c0, v);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] += in[e];
-                fetch(c0 + 32);
+                fetch(c0 + 4 * kREpi);
                 const size_t o = at + static_cast<size_t>(c0) * a.H;
                 if (wide) {
 #pragma unroll
