@@ -22,7 +22,7 @@
 //
 // One persistent block per SM.  Roles:
 //   dequantising warps, two groups that take alternate stages, read codes
-//       straight to registers two of their stages ahead (no shared memory is
+//       straight to registers one or two of their stages ahead (no shared memory is
 //       spent on codes) and write fp16 tiles to the A stages, four blocks of 32
 //       a thread between two barriers;
 //   loader warps fill the B stages: phase 1 gathers the tokens' rows with
@@ -84,7 +84,7 @@ struct Cfg {
     static constexpr int GROUP = PHASE == 1 ? 6 : 4;          // warps of a dequantising group: 4 blocks a thread
     static constexpr int DEQ = 2 * GROUP;
     static constexpr int EPI = 4;
-    static constexpr int LOAD = PHASE == 1 ? 7 : 1;           // loader warps
+    static constexpr int LOAD = PHASE == 2 ? 1 : MAXN > 64 ? 5 : 3;      // loader warps
     static constexpr int THREADS = 32 * (DEQ + EPI + 1 + LOAD);
     static constexpr uint32_t A_STAGE = NM * kMat;
     static constexpr uint32_t B_TILE = MAXN * 128;
@@ -115,39 +115,62 @@ __device__ __forceinline__ Codes<BITS> load_codes(const uint8_t *p) {
     return c;
 }
 
-// (1024 + a, 1024 + b) from the bytes of `bytes` that sel names, less 1024 and
-// the offset (exact), times the step: one rounding.
-__device__ __forceinline__ uint32_t weight2(uint32_t bytes, uint32_t sel, __half2 off, __half2 d) {
-    const uint32_t m = __byte_perm(bytes, 0x64646464u, sel);
-    __half2 h = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&m), off), d);
-    return *reinterpret_cast<uint32_t *>(&h);
+// A block's 32 values are written in the order in which its codes come out with
+// the fewest steps, two at a time from bits 16 apart: position p of the 32
+// holds value block_order(p).  Whatever meets them follows: x's columns (K of
+// g and u), Wg's and Wu's rows against q's (M of phase 1), the lanes' h (M of
+// phase 2).
+template <int BITS>
+__device__ __forceinline__ int block_order(int p) {
+    const int c = p >> 3, in4 = ((p & 1) << 1) | ((p >> 1) & 1);                // 0, 2, 1, 3
+    if (BITS == 4) return 4 * c + 4 * (p & 4) + in4;                            // + 16 in the chunk's second half
+    return 4 * (c >> 1) + 8 * (2 * (c & 1) + ((p >> 2) & 1)) + in4;
+}
+// Its inverse for four neighbouring values 4f .. 4f+3: the position of the first.
+__device__ __forceinline__ int block_place(int bits, int f) {
+    if (bits == 4) return f < 4 ? 8 * f : 8 * (f - 4) + 4;
+    return 8 * (2 * (f & 1) + (f >> 2)) + 4 * ((f >> 1) & 1);
+}
+
+// Two codes at bit SHIFT of w's halves, as fp16 weights: 1024 + 2^SHIFT q from
+// the bits, back to q less the offset (exact), times the step (one rounding).
+template <int BITS, int SHIFT>
+__device__ __forceinline__ uint32_t weight2(uint32_t w, __half2 d) {
+    constexpr uint32_t mask = ((1u << BITS) - 1) << SHIFT;
+    const uint32_t m = (w & (mask | mask << 16)) | 0x64006400u;
+    __half2 h = *reinterpret_cast<const __half2 *>(&m);
+    constexpr float unit = 1.f / (1 << SHIFT), off = 1024.f * unit + (1 << (BITS - 1));
+    if constexpr (SHIFT == 0) h = __hsub2(h, __float2half2_rn(off));
+    else h = __hfma2(h, __float2half2_rn(unit), __float2half2_rn(-off));
+    h = __hmul2(h, d);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // Writes a block's 32 values into 16-byte chunks c0 .. c0+3 of the 128-byte row
-// at `row`, chunk c at c ^ sw.  Values 8j..8j+7 go to chunk j; with FLIP the
-// two halves are written in the other order (the same bytes), which keeps the
-// lanes of a quarter warp on different banks where two of them write the same
-// chunk of different tiles.
+// at `row`, chunk c at c ^ sw, in block_order.  With FLIP the two halves are
+// written in the other order (the same bytes), which keeps the lanes of a
+// quarter warp on different banks where two of them write the same chunk of
+// different tiles.
 template <int BITS>
-__device__ __forceinline__ void put_block(Codes<BITS> c, __half d, uint32_t row, int c0, int sw, bool flip) {
-    const __half2 d2 = __half2half2(d), off = __float2half2_rn(BITS == 4 ? 1032.f : 1026.f);
-    if (flip) {
-#pragma unroll
-        for (int i = 0; i < BITS; ++i) c.w[i] = ((c.w[i] >> 4) & 0x0F0F0F0Fu) | ((c.w[i] << 4) & 0xF0F0F0F0u);
-    }
+__device__ __forceinline__ void put_block(const Codes<BITS> &c, __half d, uint32_t row, int c0, int sw, bool flip) {
+    const __half2 d2 = __half2half2(d);
     const int x = flip ? sw ^ 2 : sw;
+    if constexpr (BITS == 4) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t lo, hi;                       // values 8j..8j+3 and 8j+4..8j+7, one per byte
-        if constexpr (BITS == 4) {
-            lo = (j < 2 ? c.w[2 * j] : c.w[2 * j - 4] >> 4) & 0x0F0F0F0Fu;
-            hi = (j < 2 ? c.w[2 * j + 1] : c.w[2 * j - 3] >> 4) & 0x0F0F0F0Fu;
-        } else {
-            lo = (c.w[0] >> (2 * j)) & 0x03030303u;
-            hi = (c.w[1] >> (2 * j)) & 0x03030303u;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = flip ? c.w[j ^ 2] : c.w[j], v = w >> 8;
+            st_shared16(row + (((c0 + j) ^ x) << 4), weight2<4, 0>(w, d2), weight2<4, 0>(v, d2), weight2<4, 4>(w, d2),
+                        weight2<4, 4>(v, d2));
         }
-        st_shared16(row + (((c0 + j) ^ x) << 4), weight2(lo, 0x5140u, off, d2), weight2(lo, 0x5342u, off, d2),
-                    weight2(hi, 0x5140u, off, d2), weight2(hi, 0x5342u, off, d2));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t w = flip ? c.w[j ^ 1] : c.w[j], v = w >> 8;
+            st_shared16(row + (((c0 + 2 * j) ^ x) << 4), weight2<2, 0>(w, d2), weight2<2, 0>(v, d2), weight2<2, 2>(w, d2),
+                        weight2<2, 2>(v, d2));
+            st_shared16(row + (((c0 + 2 * j + 1) ^ x) << 4), weight2<2, 4>(w, d2), weight2<2, 4>(v, d2),
+                        weight2<2, 6>(w, d2), weight2<2, 6>(v, d2));
+        }
     }
 }
 
@@ -259,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
                 const bool up = PHASE == 2 && st * C::KSTAGE >= I;
                 const uint8_t *codes = PHASE == 2 ? (up ? bv.cu : bv.cg) : mat == 0 ? bv.cg : mat == 1 ? bv.cu : bv.cd;
                 const __half *steps = PHASE == 2 ? (up ? bv.su : bv.sg) : mat == 0 ? bv.sg : mat == 1 ? bv.su : bv.sd;
-                const size_t row = trans ? st * C::KSTAGE - (up ? I : 0) + r : m0 + r;
+                const size_t row = trans ? st * C::KSTAGE - (up ? I : 0) + r : m0 + block_order<BITS>(r);
                 const int col = trans ? m0 / 32 + b : 2 * group + b;
                 cp = codes + row * rowb + col * BB;
                 sp = reinterpret_cast<const unsigned short *>(steps) + row * rows + col;
@@ -296,15 +319,27 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
             if (sa >= SA) sa -= SA, phase ^= 1;
             return true;
         };
-        Step<BITS> s0, s1;
         const int n = n_my * (nk / 2);
-        if (n > 0) fetch(s0);
-        if (n > 1) fetch(s1);
-        for (int i = 0; i < n; i += 2) {
-            if (!put(s0)) break;
-            if (i + 2 < n) fetch(s0);
-            if (i + 1 >= n || !put(s1)) break;
-            if (i + 3 < n) fetch(s1);
+        if constexpr (PHASE == 1) {
+            // one stage ahead: the other group's stage takes longer than a load
+            // (two ahead cost registers: 1093 us against 1037 at 8192 tokens)
+            Step<BITS> s0;
+            if (n > 0) fetch(s0);
+            for (int i = 0; i < n; ++i) {
+                if (!put(s0)) break;
+                if (i + 1 < n) fetch(s0);
+            }
+        } else {
+            // two ahead: a stage is shorter here (194 us one ahead, 167 two, at 64 tokens)
+            Step<BITS> s0, s1;
+            if (n > 0) fetch(s0);
+            if (n > 1) fetch(s1);
+            for (int i = 0; i < n; i += 2) {
+                if (!put(s0)) break;
+                if (i + 2 < n) fetch(s0);
+                if (i + 1 >= n || !put(s1)) break;
+                if (i + 3 < n) fetch(s1);
+            }
         }
     } else if (PHASE == 1 && warp >= kLoad0) {
         // ------------------------------------------------- rows of x and dy
@@ -387,7 +422,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         // -------------------------------------------------------- epilogue
         static_assert(kEpi0 % 4 == 0, "TMEM lanes follow the warp's rank");
         const int ew = warp - kEpi0, q = ew & 3;              // TMEM lanes 32q .. 32q + 31
-        const int m = 32 * q + lane;
+        const int m = 32 * q + block_order<BITS>(lane);       // the weight row (column) of this lane
         // each warp has its own table of the tile's scales: no barrier among
         // them, of which one may leave early
         float *sx_s = reinterpret_cast<float *>(smem + C::OFF_SX) + ew * MAXN;
@@ -641,16 +676,18 @@ __global__ void __launch_bounds__(kPrepThreads) k_bwd_prepare(FfnBackward a, Pre
         for (int w = 0; w < kPrepThreads / 32; ++w) top = max(top, part[w]);
         const float2 sc = row_scale(top);
         scale[which] = sc;
+        // x in the order of the blocks that it meets as K of g and u
         uint2 *out = reinterpret_cast<uint2 *>((which ? p.dy16 : p.x16) + t * a.H);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int h4 = tid + i * kPrepThreads;
             if (h4 < h4n) {
-                __half2 lo = __floats2half2_rn(v[i].x * sc.x, v[i].y * sc.x), hi = __floats2half2_rn(v[i].z * sc.x, v[i].w * sc.x);
+                const float y = which ? v[i].y : v[i].z, z = which ? v[i].z : v[i].y;
+                __half2 lo = __floats2half2_rn(v[i].x * sc.x, y * sc.x), hi = __floats2half2_rn(z * sc.x, v[i].w * sc.x);
                 uint2 u;
                 u.x = *reinterpret_cast<uint32_t *>(&lo);
                 u.y = *reinterpret_cast<uint32_t *>(&hi);
-                out[h4] = u;
+                out[which ? h4 : (h4 & ~7) + block_place(a.bits, h4 & 7) / 4] = u;
             }
         }
     }
