@@ -15,10 +15,13 @@
 // are in flight in passes 2 and 3, and pass 2, which has the fewest columns and
 // the longest sums, runs in strips of 64 columns and blocks of 16 warps.  The
 // shared expert's rows come first and split over tasks: left to one task each,
-// they were the tail at 16 tokens (187 us of pass 3).
+// they were the tail at 16 tokens (187 us of pass 3).  Each pass may start
+// while the one before it runs (programmatic dependent launch) and asks for its
+// first task's codes before it waits.
 #include "common.cuh"
 #include "qdot.cuh"
 #include "train/ffn_bwd.cuh"
+#include "train/launch.cuh"
 
 namespace moe {
 
@@ -28,7 +31,7 @@ constexpr int kNT = 2;             // rows in flight
 constexpr int kLoads = 4;          // weight rows a lane has in flight in passes 2 and 3
 // Passes 2 and 3: columns of a task and warps of a block.
 template <bool DOWN> struct Strip {
-    static constexpr int COLS = DOWN ? 64 : 128, BLOCKS = COLS / 32, WARPS = DOWN ? 16 : 8, THREADS = 32 * WARPS;
+    static constexpr int COLS = DOWN ? 64 : 128, BLOCKS = COLS / 32, WARPS = 16, THREADS = 32 * WARPS;
     static constexpr int SUBS = 32 / BLOCKS;       // weight rows a warp reads at once
 };
 
@@ -85,6 +88,7 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_gateup(FfnBackward a, GemvBw
     const int n_items = n_act + chunks, row_blocks = a.I / 16;
     const int nch = a.H / Q::EPC, nsc = a.H / 32;
     const size_t rowb = static_cast<size_t>(a.H) * BITS / 8;
+    pdl_next();
     for (long task = blockIdx.x; task < static_cast<long>(n_items) * row_blocks; task += gridDim.x) {
         const int item = static_cast<int>(task / row_blocks), rb = static_cast<int>(task - static_cast<long>(item) * row_blocks);
         const Rows R = task_rows(a, item, n_act, chunks, threadIdx.x == 0 && rb == 0);
@@ -218,6 +222,22 @@ __global__ void __launch_bounds__(Strip<DOWN>::THREADS) k_bwd_columns(FfnBackwar
     const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), a.err);
     const int chunks = a.shared ? (a.T + kNT - 1) / kNT : 0;
     const int n_items = n_act + chunks, strips = C / S::COLS;
+    pdl_next();
+    if (static_cast<long>(blockIdx.x) < static_cast<long>(n_items) * strips) {
+        // the first task's codes on their way to L2: inputs of the call, not results of the pass before
+        const int item = blockIdx.x / strips, st = blockIdx.x % strips;
+        const Rows R = task_rows(a, item, n_act, chunks, false);
+        if (R.G.n > 0) {
+            const BlobView bv = blob_view(R.G.blob, BITS, a.H, a.I);
+            const size_t rowb = static_cast<size_t>(C) * BITS / 8;
+            for (int m = threadIdx.x; m < M; m += S::THREADS) {
+                const uint8_t *codes = DOWN ? bv.cd : m < a.I ? bv.cg : bv.cu;
+                const size_t row = DOWN || m < a.I ? m : m - a.I;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(codes + row * rowb + st * S::COLS * BITS / 8));
+            }
+        }
+    }
+    pdl_wait();
     for (long task = blockIdx.x; task < static_cast<long>(n_items) * strips; task += gridDim.x) {
         const int item = static_cast<int>(task / strips), st = static_cast<int>(task - static_cast<long>(item) * strips);
         const Rows R = task_rows(a, item, n_act, chunks, false);
@@ -292,6 +312,7 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, const 
                                                            const uint8_t *__restrict__ ok,
                                                            const float2 *__restrict__ scale) {
     const size_t t = blockIdx.x;
+    pdl_wait();
     const float2 sc = scale ? scale[t] : make_float2(1.f, 1.f);
     __shared__ int row_s[32];
     __shared__ float w_s[32];
@@ -388,19 +409,25 @@ static int launch_gemv_bwd(const FfnBackward &a, const GemvBwdWs &w, cudaStream_
     if (!rc) rc = smem(reinterpret_cast<const void *>(k_bwd_columns<BITS, false>), sm3);
     if (rc) return rc;
     k_bwd_gateup<BITS><<<grid(a.I / 16), kBwThreads, sm1, s>>>(a, w);
-    k_bwd_columns<BITS, true><<<grid(a.I / D::COLS), D::THREADS, sm2, s>>>(a, w);
-    k_bwd_columns<BITS, false><<<grid(a.H / U::COLS), U::THREADS, sm3, s>>>(a, w);
-    count_launches(3);
+    count_launches(1);
     rc = cuda_status(cudaGetLastError(), "expert backward launch");
     if (rc) return rc;
+    rc = cuda_status(launch_after(k_bwd_columns<BITS, true>, dim3(grid(a.I / D::COLS)), D::THREADS, sm2, s, a, w),
+                     "expert backward launch");
+    if (rc) return rc;
+    rc = cuda_status(launch_after(k_bwd_columns<BITS, false>, dim3(grid(a.H / U::COLS)), U::THREADS, sm3, s, a, w),
+                     "expert backward launch");
+    if (rc) return rc;
+    count_launches(2);
     return launch_ffn_backward_gather(a, w.dxp, w.dwp, a.I / D::COLS, w.ok, nullptr, s);
 }
 
 int launch_ffn_backward_gather(const FfnBackward &a, const float *dxp, const float *dwp, int shares,
                                const uint8_t *ok, const float2 *scale, cudaStream_t s) {
-    k_bwd_gather<<<a.T, kBwThreads, 0, s>>>(a, dxp, dwp, shares, ok, scale);
-    count_launches(1);
-    return cuda_status(cudaGetLastError(), "expert backward gather launch");
+    const int rc = cuda_status(launch_after(k_bwd_gather, dim3(a.T), kBwThreads, 0, s, a, dxp, dwp, shares, ok, scale),
+                               "expert backward gather launch");
+    if (!rc) count_launches(1);
+    return rc;
 }
 
 int launch_ffn_backward_gemv(const FfnBackward &a, void *ws, cudaStream_t s) {

@@ -34,6 +34,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "train/ffn_bwd.cuh"
+#include "train/launch.cuh"
 #include "train/tma.cuh"
 #include "train/umma.cuh"
 
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    pdl_wait();                                               // the lists and rows of the kernel before
     // tiles: all weight rows of a token tile first, dealt to blocks round robin
     const int total = *p.n_tiles * MT, grid = static_cast<int>(gridDim.x), bid = static_cast<int>(blockIdx.x);
     const int n_my = bid < total ? (total - 1 - bid) / grid + 1 : 0;
@@ -575,6 +577,7 @@ constexpr int kPrepThreads = 256;
 struct Prep {
     __half *x16, *dy16;
     float2 *scale;
+    uint8_t *ok;
     TokTile *tiles1, *tiles2;
     int *counts;                  // token tiles of phase 1 and 2
     int max1, max2;               // tokens per tile
@@ -601,8 +604,10 @@ __device__ __forceinline__ int tile_rows(int n, int most) {
 
 // Block 0 lists both phases' token tiles; each other block scales and rounds
 // one token's x and dy.
+// V: float4 a thread holds of a row.
+template <int V>
 __global__ void __launch_bounds__(kPrepThreads) k_bwd_prepare(FfnBackward a, Prep p) {
-    __shared__ uint32_t part[kPrepThreads / 32];
+    __shared__ uint32_t part[2][kPrepThreads / 32];
     __shared__ int3 sums[kPrepThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (blockIdx.x == 0) {
@@ -644,51 +649,56 @@ __global__ void __launch_bounds__(kPrepThreads) k_bwd_prepare(FfnBackward a, Pre
             for (int i = 0; i < c.y; ++i)
                 p.tiles2[at.y + i] = {G.blob, G.row0, i * r.y, min(r.y, G.n - i * r.y), at.z + i * r.y, {0, 0}};
         }
+        pdl_next();
         const bool fits = done.x <= p.cap1 && done.y <= p.cap2 && done.z <= p.cols;
         if (tid == 0) p.counts[0] = fits ? done.x : 0, p.counts[1] = fits ? done.y : 0;
         return;
     }
+    pdl_next();
     const size_t t = blockIdx.x - 1;
     const int h4n = a.H / 4;
-    constexpr int V = 8192 / 4 / kPrepThreads;
-    float2 scale[2];
-#pragma unroll 1
+    if (tid < a.k) p.ok[t * a.k + tid] = 0;
+    float4 v[2][V];                                           // x and dy, both rows' loads in flight
+    uint32_t top[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int h4 = tid + i * kPrepThreads;
+        if (h4 >= h4n) continue;
+        v[0][i] = bwd_load4(a.x, a.x_scales, a.x_dtype, t, a.H, h4);
+        v[1][i] = bwd_load4(a.dy, nullptr, a.dy_dtype, t, a.H, h4);
+    }
+#pragma unroll
     for (int which = 0; which < 2; ++which) {
-        const void *src = which ? a.dy : a.x;
-        const uint8_t *steps = which ? nullptr : a.x_scales;
-        const int kind = which ? a.dy_dtype : a.x_dtype;
-        float4 v[V];
-        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int h4 = tid + i * kPrepThreads;
-            if (h4 < h4n) {
-                v[i] = bwd_load4(src, steps, kind, t, a.H, h4);
-                top = max(max(top, __float_as_uint(fabsf(v[i].x))), __float_as_uint(fabsf(v[i].y)));
-                top = max(max(top, __float_as_uint(fabsf(v[i].z))), __float_as_uint(fabsf(v[i].w)));
-            }
+            if (tid + i * kPrepThreads >= h4n) continue;
+            const float4 &u = v[which][i];
+            top[which] = max(max(top[which], __float_as_uint(fabsf(u.x))), __float_as_uint(fabsf(u.y)));
+            top[which] = max(max(top[which], __float_as_uint(fabsf(u.z))), __float_as_uint(fabsf(u.w)));
         }
-        top = __reduce_max_sync(0xffffffffu, top);
-        __syncthreads();
-        if (lane == 0) part[warp] = top;
-        __syncthreads();
+        top[which] = __reduce_max_sync(0xffffffffu, top[which]);
+        if (lane == 0) part[which][warp] = top[which];
+    }
+    __syncthreads();
+    float2 scale[2];
 #pragma unroll
-        for (int w = 0; w < kPrepThreads / 32; ++w) top = max(top, part[w]);
-        const float2 sc = row_scale(top);
-        scale[which] = sc;
+    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+        for (int w = 0; w < kPrepThreads / 32; ++w) top[which] = max(top[which], part[which][w]);
+        const float2 sc = scale[which] = row_scale(top[which]);
         // x in the order of the blocks that it meets as K of g and u
         uint2 *out = reinterpret_cast<uint2 *>((which ? p.dy16 : p.x16) + t * a.H);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int h4 = tid + i * kPrepThreads;
-            if (h4 < h4n) {
-                const float y = which ? v[i].y : v[i].z, z = which ? v[i].z : v[i].y;
-                __half2 lo = __floats2half2_rn(v[i].x * sc.x, y * sc.x), hi = __floats2half2_rn(z * sc.x, v[i].w * sc.x);
-                uint2 u;
-                u.x = *reinterpret_cast<uint32_t *>(&lo);
-                u.y = *reinterpret_cast<uint32_t *>(&hi);
-                out[which ? h4 : (h4 & ~7) + block_place(a.bits, h4 & 7) / 4] = u;
-            }
+            if (h4 >= h4n) continue;
+            const float4 &u = v[which][i];
+            const float y = which ? u.y : u.z, z = which ? u.z : u.y;
+            __half2 lo = __floats2half2_rn(u.x * sc.x, y * sc.x), hi = __floats2half2_rn(z * sc.x, u.w * sc.x);
+            uint2 o;
+            o.x = *reinterpret_cast<uint32_t *>(&lo);
+            o.y = *reinterpret_cast<uint32_t *>(&hi);
+            out[which ? h4 : (h4 & ~7) + block_place(a.bits, h4 & 7) / 4] = o;
         }
     }
     if (tid == 0) p.scale[t] = make_float2(scale[0].y, scale[1].y);
@@ -758,9 +768,10 @@ int launch_phase(const TcArgs &p, const CUtensorMap &map, cudaStream_t s) {
                                               static_cast<int>(C::SMEM)),
                          "backward gemm smem attribute");
     if (rc) return rc;
-    k_bwd_tc<BITS, PHASE, MAXN><<<num_sms(), C::THREADS, C::SMEM, s>>>(p, map);
-    count_launches(1);
-    return cuda_status(cudaGetLastError(), "backward gemm launch");
+    rc = cuda_status(launch_after(k_bwd_tc<BITS, PHASE, MAXN>, dim3(num_sms()), C::THREADS, C::SMEM, s, p, map),
+                     "backward gemm launch");
+    if (!rc) count_launches(1);
+    return rc;
 }
 }  // namespace
 
@@ -778,14 +789,13 @@ int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     TcWs w;
     carve(a.T, a.k, a.H, a.I, a.E, static_cast<uint8_t *>(ws), &w);
     const TcPlan plan = plan_of(a.T, a.k, a.E);
-    int rc = cuda_status(cudaMemsetAsync(w.ok, 0, static_cast<size_t>(a.T) * a.k, s), "row flags memset");
-    if (rc) return rc;
-    const Prep prep = {w.x16, w.dy16, w.scale, w.tiles1, w.tiles2, w.counts, plan.max1, plan.max2,
+    const Prep prep = {w.x16, w.dy16, w.scale, w.ok, w.tiles1, w.tiles2, w.counts, plan.max1, plan.max2,
                        static_cast<int>(plan.tiles1), static_cast<int>(plan.tiles2),
                        static_cast<int>(plan.cols)};
-    k_bwd_prepare<<<a.T + 1, kPrepThreads, 0, s>>>(a, prep);
+    if (a.H <= 2048) k_bwd_prepare<2><<<a.T + 1, kPrepThreads, 0, s>>>(a, prep);
+    else k_bwd_prepare<8><<<a.T + 1, kPrepThreads, 0, s>>>(a, prep);
     count_launches(1);
-    rc = cuda_status(cudaGetLastError(), "backward prepare launch");
+    int rc = cuda_status(cudaGetLastError(), "backward prepare launch");
     if (rc) return rc;
     const long hook = static_cast<long>(test_hook_value(MOE_HOOK_GEMM_SPIN));
     TcArgs p = {a, w.scale, w.gu16, static_cast<int>(plan.cols), w.x16, w.dy16, w.dwp, w.dxp, w.ok, w.tiles1, w.counts, hook > 0 ? hook : kSpin};
