@@ -17,7 +17,9 @@
  * status codes and moe_last_error(), device pointers 16-byte aligned unless
  * stated otherwise, all memory owned by the caller, problems met on the device
  * reported in the device error word.  No call keeps anything between calls;
- * results do not depend on scheduling (no floating-point atomics).  Two calls
+ * results do not depend on scheduling (no floating-point atomics).  The waits
+ * inside the tensor-core kernels end after a second (the test hook
+ * MOE_HOOK_WAIT_LIMIT_NS limits these too) with MOE_DEVERR_TIMEOUT.  Two calls
  * that overlap on the GPU must not share a workspace, which is scratch only:
  * it needs no initial contents.
  */
@@ -110,7 +112,7 @@ int moe_route_backward(const float *logits, const int32_t *topk_ids, const float
  *           own (undone in fp32 at the end), so that neither's scale matters;
  *           the gradients of g and u are rounded to fp16 between the two
  *           products.  fp32 accumulation.  Blobs in device memory.
- *           MOE_MODE_AUTO: GEMV up to 6 tokens, else GEMM.
+ *           MOE_MODE_AUTO: GEMV up to 4 tokens, else GEMM.
  *  Shapes as for moe_expert_ffn_*: H a multiple of 128 up to 8192, I up to 4096.
  *  ws: at least moe_expert_ffn_backward_ws_size(...) bytes. */
 size_t moe_expert_ffn_backward_ws_size(int bits, int T, int k, int H, int I, int E, int mode);

@@ -1,23 +1,22 @@
 // Backward pass of the quantized experts on CUDA cores, fp32 throughout
 // (MOE_MODE_GEMV): a few tokens, where reading the weights is the cost.
 //
-// Three passes over an expert's weights' codes, for one or two rows at a time:
-//   1. g = Wg x, u = Wu x                       (dot products along a row)
-//   2. q = Wd^T dy, then dg, du and the strip's share of <q, h>   (columns)
-//   3. dxp = Wg^T dg + Wu^T du                                    (columns)
-// and a gather of each token's rows, weighted by its gates.  Passes 2 and 3
-// read a row's codes as they lie, two (pass 2) or four neighbouring blocks a
-// row, each lane keeping the 32 sums of its block's columns in registers;
-// lanes and warps are joined once at the end.  A weight is decoded exactly
-// (code minus offset is a small whole number) and once for the rows in flight.
+// Two passes over an expert's weights' codes, for one or two rows at a time:
+//   1. g = Wg x, u = Wu x (dot products along a row) and q = Wd^T dy (columns),
+//      tasks of one launch, since neither needs the other
+//   2. dg, du from them, then dxp = Wg^T dg + Wu^T du             (columns)
+// and a gather of each token's rows, weighted by its gates.  Columns are summed
+// over rows of codes as they lie, two (q) or four neighbouring blocks a row,
+// each lane keeping the 32 sums of its block's columns in registers; lanes and
+// warps are joined once at the end.  A weight is decoded exactly (code minus
+// offset is a small whole number) and once for the rows in flight.
 //
-// At one token the passes are chains of memory latencies: four loads a lane
-// are in flight in passes 2 and 3, and pass 2, which has the fewest columns and
-// the longest sums, runs in strips of 64 columns and blocks of 16 warps.  The
-// shared expert's rows come first and split over tasks: left to one task each,
-// they were the tail at 16 tokens (187 us of pass 3).  Each pass may start
-// while the one before it runs (programmatic dependent launch) and asks for its
-// first task's codes before it waits.
+// At one token this is a chain of memory latencies and launches: three kernels,
+// each of which may start while the one before it runs (programmatic dependent
+// launch).  (With q a pass of its own and a memset in front: 41 us at one
+// token, 512 experts, top-10; an L2 prefetch of the first codes before the wait
+// changed nothing.)  The shared expert's rows come first and split over tasks:
+// left to one task each, they were the tail at 16 tokens.
 #include "common.cuh"
 #include "qdot.cuh"
 #include "train/ffn_bwd.cuh"
@@ -28,16 +27,18 @@ namespace moe {
 namespace {
 constexpr int kBwThreads = 256;
 constexpr int kNT = 2;             // rows in flight
-constexpr int kLoads = 4;          // weight rows a lane has in flight in passes 2 and 3
-// Passes 2 and 3: columns of a task and warps of a block.
+constexpr int kLoads = 2;          // weight rows a lane has in flight in column sums
+// Column sums: columns of a task (64 of Wd, which has the fewest and the longest
+// sums, 128 of Wg and Wu).
 template <bool DOWN> struct Strip {
-    static constexpr int COLS = DOWN ? 64 : 128, BLOCKS = COLS / 32, WARPS = 16, THREADS = 32 * WARPS;
+    static constexpr int COLS = DOWN ? 64 : 128, BLOCKS = COLS / 32;
     static constexpr int SUBS = 32 / BLOCKS;       // weight rows a warp reads at once
 };
+constexpr int kBwWarps = kBwThreads / 32;
 
 struct GemvBwdWs {
-    float *gu;      // [T*k + T, 2I]: g, u, then dg, du
-    float *dwp;     // [T*k, I / 64]: shares of <q, h>
+    float *guq;     // [T*k + T, 3I]: g, u, q
+    float *dwp;     // [T*k]: <q, h>
     float *dxp;     // [T*k + T, H]
     uint8_t *ok;    // [T*k]: the row's expert was computed
 };
@@ -76,83 +77,71 @@ __device__ __forceinline__ Rows task_rows(const FfnBackward &a, int item, int n_
 }
 }  // namespace
 
-// Pass 1.  Task = (group, 16 weight rows): a warp takes two rows of both
-// matrices, its lanes the row's chunks of 16 bytes.
+// Pass 1, gate and up: 16 weight rows of both matrices, a warp two of each, its
+// lanes the row's chunks of 16 bytes.
 template <int BITS>
-__global__ void __launch_bounds__(kBwThreads) k_bwd_gateup(FfnBackward a, GemvBwdWs ws) {
-    using Q = QT<BITS>;
-    extern __shared__ float4 xs[];                 // [kNT][piece][chunk]
+__device__ __forceinline__ void gate_up(const FfnBackward &a, const GemvBwdWs &ws, const Rows &R, int rb, float4 *xs) {
+    using Q = QT<BITS>;                            // xs: [kNT][piece][chunk]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), a.err);
-    const int chunks = a.shared ? (a.T + kNT - 1) / kNT : 0;
-    const int n_items = n_act + chunks, row_blocks = a.I / 16;
     const int nch = a.H / Q::EPC, nsc = a.H / 32;
     const size_t rowb = static_cast<size_t>(a.H) * BITS / 8;
-    pdl_next();
-    for (long task = blockIdx.x; task < static_cast<long>(n_items) * row_blocks; task += gridDim.x) {
-        const int item = static_cast<int>(task / row_blocks), rb = static_cast<int>(task - static_cast<long>(item) * row_blocks);
-        const Rows R = task_rows(a, item, n_act, chunks, threadIdx.x == 0 && rb == 0);
-        const BwdGroup G = R.G;
-        if (G.n <= 0) continue;
-        const BlobView bv = blob_view(G.blob, BITS, a.H, a.I);
-        const int i0 = rb * 16 + warp * 2;
-        if (rb == 0 && G.row0 >= 0)
-            for (int r = threadIdx.x; r < G.n; r += kBwThreads) ws.ok[G.row0 + r] = 1;
-        const size_t out0 = G.row0 >= 0 ? G.row0 : static_cast<size_t>(a.T) * a.k;
-        for (int r0 = R.r0; r0 < R.r1; r0 += kNT) {
-            __syncthreads();
-            for (int t = 0; t < kNT; ++t) {
-                const bool in = r0 + t < G.n;
-                const size_t tok = in ? bwd_token(a, G, r0 + t) : 0;
-                for (int h4 = threadIdx.x; h4 < a.H / 4; h4 += kBwThreads)
-                    xs[(t * Q::PPC + h4 % Q::PPC) * nch + h4 / Q::PPC] =
-                        in ? bwd_load4(a.x, a.x_scales, a.x_dtype, tok, a.H, h4) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            __syncthreads();
-            float dot[4][kNT] = {};
-            for (int cc = lane; cc < nch; cc += 32) {
-                uint4 code[4];
-                float d[4][Q::BPC];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const size_t i = i0 + (v >> 1);
-                    code[v] = ldg_stream((v & 1 ? bv.cu : bv.cg) + i * rowb + static_cast<size_t>(cc) * 16);
-                    load_scales<BITS>((v & 1 ? bv.su : bv.sg) + i * nsc, cc, true, d[v]);
-                }
-#pragma unroll
-                for (int b = 0; b < Q::BPC; ++b) {
-                    float acc[4][kNT] = {};
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        float4 x[kNT];
-#pragma unroll
-                        for (int t = 0; t < kNT; ++t) x[t] = xs[(t * Q::PPC + 8 * b + p) * nch + cc];
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const uint32_t words[4] = {code[v].x, code[v].y, code[v].z, code[v].w};
-                            float w[4];
-                            decode4<BITS>(block_piece<BITS>(words + (BITS == 4 ? 0 : 2 * b), p), w);
-#pragma unroll
-                            for (int t = 0; t < kNT; ++t)
-                                acc[v][t] = fmaf(w[3], x[t].w, fmaf(w[2], x[t].z,
-                                            fmaf(w[1], x[t].y, fmaf(w[0], x[t].x, acc[v][t]))));
-                        }
-                    }
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-#pragma unroll
-                        for (int t = 0; t < kNT; ++t) dot[v][t] = fmaf(d[v][b], acc[v][t], dot[v][t]);
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-#pragma unroll
-                for (int t = 0; t < kNT; ++t) {
-                    const float s = warp_sum(dot[v][t]);
-                    if (lane == 0 && r0 + t < G.n)
-                        ws.gu[(out0 + r0 + t) * 2 * a.I + (v & 1) * a.I + i0 + (v >> 1)] = s;
-                }
+    const BwdGroup G = R.G;
+    const BlobView bv = blob_view(G.blob, BITS, a.H, a.I);
+    const int i0 = rb * 16 + warp * 2;
+    const size_t out0 = G.row0 >= 0 ? G.row0 : static_cast<size_t>(a.T) * a.k;
+    for (int r0 = R.r0; r0 < R.r1; r0 += kNT) {
+        __syncthreads();
+        for (int t = 0; t < kNT; ++t) {
+            const bool in = r0 + t < R.r1;
+            const size_t tok = in ? bwd_token(a, G, r0 + t) : 0;
+            for (int h4 = threadIdx.x; h4 < a.H / 4; h4 += kBwThreads)
+                xs[(t * Q::PPC + h4 % Q::PPC) * nch + h4 / Q::PPC] =
+                    in ? bwd_load4(a.x, a.x_scales, a.x_dtype, tok, a.H, h4) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        __syncthreads();
+        float dot[4][kNT] = {};
+        for (int cc = lane; cc < nch; cc += 32) {
+            uint4 code[4];
+            float d[4][Q::BPC];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const size_t i = i0 + (v >> 1);
+                code[v] = ldg_stream((v & 1 ? bv.cu : bv.cg) + i * rowb + static_cast<size_t>(cc) * 16);
+                load_scales<BITS>((v & 1 ? bv.su : bv.sg) + i * nsc, cc, true, d[v]);
+            }
+#pragma unroll
+            for (int b = 0; b < Q::BPC; ++b) {
+                float acc[4][kNT] = {};
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    float4 x[kNT];
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) x[t] = xs[(t * Q::PPC + 8 * b + p) * nch + cc];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const uint32_t words[4] = {code[v].x, code[v].y, code[v].z, code[v].w};
+                        float w[4];
+                        decode4<BITS>(block_piece<BITS>(words + (BITS == 4 ? 0 : 2 * b), p), w);
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t)
+                            acc[v][t] = fmaf(w[3], x[t].w, fmaf(w[2], x[t].z,
+                                        fmaf(w[1], x[t].y, fmaf(w[0], x[t].x, acc[v][t]))));
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) dot[v][t] = fmaf(d[v][b], acc[v][t], dot[v][t]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) {
+                const float s = warp_sum(dot[v][t]);
+                if (lane == 0 && r0 + t < R.r1)
+                    ws.guq[(out0 + r0 + t) * 3 * a.I + (v & 1) * a.I + i0 + (v >> 1)] = s;
+            }
     }
 }
 
@@ -165,7 +154,7 @@ __device__ __forceinline__ void column_sums(const BlobView &bv, const float *vs,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane % S::BLOCKS, sub = lane / S::BLOCKS;
     const size_t rowb = static_cast<size_t>(C) * BITS / 8;
     const size_t cofs = static_cast<size_t>(col0 / 32 + blk) * 4 * BITS;
-    constexpr int STEP = S::SUBS * S::WARPS;
+    constexpr int STEP = S::SUBS * kBwWarps;
     for (int m0 = S::SUBS * warp + sub; m0 < M; m0 += kLoads * STEP) {
         uint32_t w[kLoads][BITS];
         float d[kLoads];
@@ -207,36 +196,93 @@ __device__ __forceinline__ void column_sums(const BlobView &bv, const float *vs,
     }
 }
 
-// Passes 2 (DOWN: columns of Wd, along h) and 3 (columns of Wg, then Wu, along
-// i).  Task = (rows, strip of columns).
-template <int BITS, bool DOWN>
-__global__ void __launch_bounds__(Strip<DOWN>::THREADS) k_bwd_columns(FfnBackward a, GemvBwdWs ws) {
-    using S = Strip<DOWN>;
-    extern __shared__ float4 vmem[];
-    const int M = DOWN ? a.H : 2 * a.I;            // rows summed over
-    const int C = DOWN ? a.I : a.H;                // columns of the matrix
-    float *vs = reinterpret_cast<float *>(vmem);   // [kNT][M]
-    float *red = vs + kNT * M;                     // [warp][kNT][COLS]
-    __shared__ float wsum[kNT * S::COLS / 32];
+// Column sums of the rows staged in vs, joined over the block: out(t, column,
+// sum) for each row in flight and column of the strip.
+template <int BITS, bool DOWN, class Out>
+__device__ __forceinline__ void columns(const BlobView &bv, const float *vs, float *red, int nt, int M, int C, int I,
+                                        int col0, Out out) {
+    using S = Strip<DOWN>;                         // red: [warp][kNT][COLS]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane % S::BLOCKS, sub = lane / S::BLOCKS;
-    const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), a.err);
-    const int chunks = a.shared ? (a.T + kNT - 1) / kNT : 0;
-    const int n_items = n_act + chunks, strips = C / S::COLS;
-    pdl_next();
-    if (static_cast<long>(blockIdx.x) < static_cast<long>(n_items) * strips) {
-        // the first task's codes on their way to L2: inputs of the call, not results of the pass before
-        const int item = blockIdx.x / strips, st = blockIdx.x % strips;
-        const Rows R = task_rows(a, item, n_act, chunks, false);
-        if (R.G.n > 0) {
-            const BlobView bv = blob_view(R.G.blob, BITS, a.H, a.I);
-            const size_t rowb = static_cast<size_t>(C) * BITS / 8;
-            for (int m = threadIdx.x; m < M; m += S::THREADS) {
-                const uint8_t *codes = DOWN ? bv.cd : m < a.I ? bv.cg : bv.cu;
-                const size_t row = DOWN || m < a.I ? m : m - a.I;
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(codes + row * rowb + st * S::COLS * BITS / 8));
-            }
+    float acc[kNT][32] = {};
+    if (nt == 1) column_sums<BITS, DOWN, 1>(bv, vs, M, C, I, col0, acc);
+    else column_sums<BITS, DOWN, kNT>(bv, vs, M, C, I, col0, acc);
+#pragma unroll
+    for (int t = 0; t < kNT; ++t) {
+        if (t >= nt) break;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            float v = acc[t][j];
+#pragma unroll
+            for (int o = S::BLOCKS; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (sub == j % S::SUBS) red[(warp * kNT + t) * S::COLS + 32 * blk + j] = v;
         }
     }
+    __syncthreads();
+    const int t = threadIdx.x / S::COLS, c = threadIdx.x % S::COLS;
+    if (t < nt) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kBwWarps; ++w) v += red[(w * kNT + t) * S::COLS + c];
+        out(t, c, v);
+    }
+}
+
+// Pass 1.  Tasks: first (rows, strip of Wd's columns), the longer ones, then
+// (rows, 16 rows of Wg and Wu).
+template <int BITS>
+__global__ void __launch_bounds__(kBwThreads) k_bwd_first(FfnBackward a, GemvBwdWs ws) {
+    using S = Strip<true>;
+    extern __shared__ float4 mem[];                // x, or dy [kNT][H] and the joining sums
+    const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), a.err);
+    const int chunks = a.shared ? (a.T + kNT - 1) / kNT : 0;
+    const int n_items = n_act + chunks, strips = a.I / S::COLS, row_blocks = a.I / 16;
+    pdl_next();
+    for (long r = static_cast<long>(blockIdx.x) * kBwThreads + threadIdx.x; r < static_cast<long>(a.T) * a.k;
+         r += static_cast<long>(gridDim.x) * kBwThreads)
+        ws.ok[r] = 0;                              // pass 2 marks the rows it computes
+    const long n_q = static_cast<long>(n_items) * strips, n_all = n_q + static_cast<long>(n_items) * row_blocks;
+    for (long task = blockIdx.x; task < n_all; task += gridDim.x) {
+        const bool down = task < n_q;
+        const long v = down ? task : task - n_q;
+        const int per = down ? strips : row_blocks;
+        const int item = static_cast<int>(v / per), part = static_cast<int>(v - static_cast<long>(item) * per);
+        const Rows R = task_rows(a, item, n_act, chunks, threadIdx.x == 0 && down && part == 0);
+        if (R.G.n <= 0) continue;
+        if (!down) {
+            gate_up<BITS>(a, ws, R, part, mem);
+            continue;
+        }
+        const BlobView bv = blob_view(R.G.blob, BITS, a.H, a.I);
+        const size_t out0 = R.G.row0 >= 0 ? R.G.row0 : static_cast<size_t>(a.T) * a.k;
+        float *vs = reinterpret_cast<float *>(mem);
+        for (int r0 = R.r0; r0 < R.r1; r0 += kNT) {
+            const int nt = min(kNT, R.r1 - r0);
+            __syncthreads();
+            for (int t = 0; t < nt; ++t) {
+                const size_t tok = bwd_token(a, R.G, r0 + t);
+                for (int h4 = threadIdx.x; h4 < a.H / 4; h4 += kBwThreads)
+                    reinterpret_cast<float4 *>(vs + t * a.H)[h4] = bwd_load4(a.dy, nullptr, a.dy_dtype, tok, a.H, h4);
+            }
+            __syncthreads();
+            columns<BITS, true>(bv, vs, vs + kNT * a.H, nt, a.H, a.I, a.I, part * S::COLS, [&](int t, int c, float q) {
+                ws.guq[(out0 + r0 + t) * 3 * a.I + 2 * a.I + part * S::COLS + c] = q;
+            });
+        }
+    }
+}
+
+// Pass 2.  Task = (rows, strip of Wg's and Wu's columns).
+template <int BITS>
+__global__ void __launch_bounds__(kBwThreads) k_bwd_second(FfnBackward a, GemvBwdWs ws) {
+    using S = Strip<false>;
+    extern __shared__ float4 mem[];
+    float *vs = reinterpret_cast<float *>(mem);    // [kNT][2I]: dg, du
+    __shared__ float wsum[kBwWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, M = 2 * a.I;
+    const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), a.err);
+    const int chunks = a.shared ? (a.T + kNT - 1) / kNT : 0;
+    const int n_items = n_act + chunks, strips = a.H / S::COLS;
+    pdl_next();
     pdl_wait();
     for (long task = blockIdx.x; task < static_cast<long>(n_items) * strips; task += gridDim.x) {
         const int item = static_cast<int>(task / strips), st = static_cast<int>(task - static_cast<long>(item) * strips);
@@ -247,59 +293,34 @@ __global__ void __launch_bounds__(Strip<DOWN>::THREADS) k_bwd_columns(FfnBackwar
         const size_t out0 = G.row0 >= 0 ? G.row0 : static_cast<size_t>(a.T) * a.k;
         for (int r0 = R.r0; r0 < R.r1; r0 += kNT) {
             const int nt = min(kNT, R.r1 - r0);
-            __syncthreads();
             for (int t = 0; t < nt; ++t) {
-                const size_t tok = DOWN ? bwd_token(a, G, r0 + t) : 0;
-                for (int m4 = threadIdx.x; m4 < M / 4; m4 += S::THREADS)
-                    reinterpret_cast<float4 *>(vs + t * M)[m4] =
-                        DOWN ? bwd_load4(a.dy, nullptr, a.dy_dtype, tok, a.H, m4)
-                             : load4(ws.gu + (out0 + r0 + t) * 2 * a.I + 4 * m4);
-            }
-            __syncthreads();
-            float acc[kNT][32] = {};
-            if (nt == 1) column_sums<BITS, DOWN, 1>(bv, vs, M, C, a.I, st * S::COLS, acc);
-            else column_sums<BITS, DOWN, kNT>(bv, vs, M, C, a.I, st * S::COLS, acc);
-#pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-                if (t >= nt) break;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float v = acc[t][j];
-#pragma unroll
-                    for (int o = S::BLOCKS; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    if (sub == j % S::SUBS) red[(warp * kNT + t) * S::COLS + 32 * blk + j] = v;
-                }
-            }
-            __syncthreads();
-            // one thread per (row in flight, column)
-            const int t = threadIdx.x / S::COLS, c = threadIdx.x % S::COLS;
-            const bool in = t < nt;
-            float v = 0.f;
-            if (in) {
-#pragma unroll
-                for (int w = 0; w < S::WARPS; ++w) v += red[(w * kNT + t) * S::COLS + c];
-            }
-            if constexpr (DOWN) {
-                float share = 0.f;
-                if (in) {
-                    float *gu = ws.gu + (out0 + r0 + t) * 2 * a.I + st * S::COLS + c;
-                    const float gv = gu[0], uv = gu[a.I], s = 1.f / (1.f + expf(-gv)), act = gv * s;
-                    gu[0] = v * uv * fmaf(act, 1.f - s, s);
-                    gu[a.I] = v * act;
-                    share = v * act * uv;
-                }
-                share = warp_sum(share);
-                if (lane == 0 && warp < kNT * S::COLS / 32) wsum[warp] = share;
+                const float *guq = ws.guq + (out0 + r0 + t) * 3 * a.I;
                 __syncthreads();
-                if (c == 0 && in && G.row0 >= 0) {
-                    float sum = 0.f;
-#pragma unroll
-                    for (int w = 0; w < S::COLS / 32; ++w) sum += wsum[t * (S::COLS / 32) + w];
-                    ws.dwp[(out0 + r0 + t) * strips + st] = sum;
+                float share = 0.f;
+                for (int i = threadIdx.x; i < a.I; i += kBwThreads) {
+                    const float g = guq[i], u = guq[a.I + i], q = guq[2 * a.I + i];
+                    const float sg = 1.f / (1.f + expf(-g)), act = g * sg;
+                    vs[t * M + i] = q * u * fmaf(act, 1.f - sg, sg);
+                    vs[t * M + a.I + i] = q * act;
+                    share = fmaf(q * act, u, share);
                 }
-            } else if (in) {
-                ws.dxp[(out0 + r0 + t) * a.H + st * S::COLS + c] = v;
+                if (st == 0 && G.row0 >= 0) {      // the same for the whole block
+                    share = warp_sum(share);
+                    if (lane == 0) wsum[warp] = share;
+                    __syncthreads();
+                    if (threadIdx.x == 0) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int w = 0; w < kBwWarps; ++w) sum += wsum[w];
+                        ws.dwp[out0 + r0 + t] = sum;
+                        ws.ok[out0 + r0 + t] = 1;
+                    }
+                }
             }
+            __syncthreads();
+            columns<BITS, false>(bv, vs, vs + kNT * M, nt, M, a.H, a.I, st * S::COLS, [&](int t, int c, float v) {
+                ws.dxp[(out0 + r0 + t) * a.H + st * S::COLS + c] = v;
+            });
         }
     }
 }
@@ -381,8 +402,8 @@ static size_t carve(int T, int k, int H, int I, uint8_t *base, GemvBwdWs *out) {
         return p;
     };
     GemvBwdWs w;
-    w.gu = reinterpret_cast<float *>(take(all * 2 * I * 4));
-    w.dwp = reinterpret_cast<float *>(take(rows * (I / Strip<true>::COLS) * 4));
+    w.guq = reinterpret_cast<float *>(take(all * 3 * I * 4));
+    w.dwp = reinterpret_cast<float *>(take(rows * 4));
     w.dxp = reinterpret_cast<float *>(take(all * H * 4));
     w.ok = take(rows);
     if (out) *out = w;
@@ -399,27 +420,23 @@ static int launch_gemv_bwd(const FfnBackward &a, const GemvBwdWs &w, cudaStream_
     auto grid = [&](long per) { return items * per < cap ? items * per : cap; };
     using D = Strip<true>;
     using U = Strip<false>;
-    const int sm1 = kNT * a.H * 4, sm2 = (kNT * a.H + D::WARPS * kNT * D::COLS) * 4;
-    const int sm3 = (kNT * 2 * a.I + U::WARPS * kNT * U::COLS) * 4;
+    static_assert(kNT * U::COLS <= kBwThreads, "a thread per row in flight and column");
+    const int sm1 = (kNT * a.H + kBwWarps * kNT * D::COLS) * 4, sm2 = (kNT * 2 * a.I + kBwWarps * kNT * U::COLS) * 4;
     auto smem = [](const void *f, int n) {
         return cuda_status(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, n), "backward smem attribute");
     };
-    int rc = smem(reinterpret_cast<const void *>(k_bwd_gateup<BITS>), sm1);
-    if (!rc) rc = smem(reinterpret_cast<const void *>(k_bwd_columns<BITS, true>), sm2);
-    if (!rc) rc = smem(reinterpret_cast<const void *>(k_bwd_columns<BITS, false>), sm3);
+    int rc = smem(reinterpret_cast<const void *>(k_bwd_first<BITS>), sm1);
+    if (!rc) rc = smem(reinterpret_cast<const void *>(k_bwd_second<BITS>), sm2);
     if (rc) return rc;
-    k_bwd_gateup<BITS><<<grid(a.I / 16), kBwThreads, sm1, s>>>(a, w);
+    k_bwd_first<BITS><<<grid(a.I / D::COLS + a.I / 16), kBwThreads, sm1, s>>>(a, w);
     count_launches(1);
     rc = cuda_status(cudaGetLastError(), "expert backward launch");
     if (rc) return rc;
-    rc = cuda_status(launch_after(k_bwd_columns<BITS, true>, dim3(grid(a.I / D::COLS)), D::THREADS, sm2, s, a, w),
+    rc = cuda_status(launch_after(k_bwd_second<BITS>, dim3(grid(a.H / U::COLS)), kBwThreads, sm2, s, a, w),
                      "expert backward launch");
     if (rc) return rc;
-    rc = cuda_status(launch_after(k_bwd_columns<BITS, false>, dim3(grid(a.H / U::COLS)), U::THREADS, sm3, s, a, w),
-                     "expert backward launch");
-    if (rc) return rc;
-    count_launches(2);
-    return launch_ffn_backward_gather(a, w.dxp, w.dwp, a.I / D::COLS, w.ok, nullptr, s);
+    count_launches(1);
+    return launch_ffn_backward_gather(a, w.dxp, w.dwp, 1, w.ok, nullptr, s);
 }
 
 int launch_ffn_backward_gather(const FfnBackward &a, const float *dxp, const float *dwp, int shares,
@@ -433,8 +450,6 @@ int launch_ffn_backward_gather(const FfnBackward &a, const float *dxp, const flo
 int launch_ffn_backward_gemv(const FfnBackward &a, void *ws, cudaStream_t s) {
     GemvBwdWs w;
     carve(a.T, a.k, a.H, a.I, static_cast<uint8_t *>(ws), &w);
-    int rc = cuda_status(cudaMemsetAsync(w.ok, 0, static_cast<size_t>(a.T) * a.k, s), "row flags memset");
-    if (rc) return rc;
     return a.bits == 4 ? launch_gemv_bwd<4>(a, w, s) : launch_gemv_bwd<2>(a, w, s);
 }
 

@@ -44,7 +44,6 @@ using namespace sm100;
 namespace {
 constexpr int kBM = 128;                    // weight rows of one product (MMA M)
 constexpr int kBK = 64;                     // K per stage: 128 bytes of fp16
-constexpr long kSpin = 1L << 22;            // polls before a wait gives up (about a second)
 constexpr uint32_t kMat = kBM * 128;        // bytes of one A tile
 constexpr size_t kSmemMax = 232448;
 
@@ -68,7 +67,7 @@ struct TcArgs {
     uint8_t *ok;                  // [T*k]
     const TokTile *tiles;         // this phase's token tiles
     const int *n_tiles;
-    long spin;
+    unsigned long long limit_ns;  // of a pipeline wait
 };
 
 // MAXN: tokens a tile holds.
@@ -239,17 +238,10 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         report(a.err, MOE_DEVERR_TIMEOUT);
         abort_s = 1;
     };
-    auto poll = [&](uint64_t *bar, uint32_t parity) {         // one thread's wait, bounded
-        if (mbar_try_wait(bar, parity)) return true;
-        for (long i = 0; i < p.spin; ++i) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if (abort_s) return false;
-        }
-        fail();
-        return false;
-    };
     auto wait = [&](uint64_t *bar, uint32_t parity) {         // a warp's wait: the same answer on every lane
-        return __all_sync(0xffffffffu, poll(bar, parity)) != 0;
+        const bool ok = mbar_wait_ns(bar, parity, p.limit_ns, &abort_s);
+        if (!ok && !abort_s) fail();
+        return __all_sync(0xffffffffu, ok) != 0;
     };
 
     if (warp < C::DEQ) {
@@ -418,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         }
         // no copy is in flight when the block leaves, also when another role gave up
         for (int f = max(0, issued - SB); f < issued; ++f)
-            for (long x = 0; x < kSpin && !mbar_try_wait(fullB + f % SB, (f / SB) & 1); ++x) {}
+            (void)mbar_wait_ns(fullB + f % SB, (f / SB) & 1, kWaitNs, nullptr);
         __syncwarp();
     } else if (warp < kMma) {
         // -------------------------------------------------------- epilogue
@@ -557,9 +549,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
             mma_commit_on(on, accF + acc);
         }
         mma_commit_on(on, drain);                             // TMEM is released once every MMA is done
-        bool done = false;
-        for (long i = 0; i < kSpin && !done; ++i) done = mbar_try_wait(drain, 0);
-        if (!done) report(a.err, MOE_DEVERR_TIMEOUT);
+        if (!mbar_wait_ns(drain, 0, kWaitNs, nullptr)) report(a.err, MOE_DEVERR_TIMEOUT);
         __syncwarp();
     }
     tc_fence_before();
@@ -797,8 +787,8 @@ int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     count_launches(1);
     int rc = cuda_status(cudaGetLastError(), "backward prepare launch");
     if (rc) return rc;
-    const long hook = static_cast<long>(test_hook_value(MOE_HOOK_GEMM_SPIN));
-    TcArgs p = {a, w.scale, w.gu16, static_cast<int>(plan.cols), w.x16, w.dy16, w.dwp, w.dxp, w.ok, w.tiles1, w.counts, hook > 0 ? hook : kSpin};
+    const long long hook = test_hook_value(MOE_HOOK_WAIT_LIMIT_NS);
+    TcArgs p = {a, w.scale, w.gu16, static_cast<int>(plan.cols), w.x16, w.dy16, w.dwp, w.dxp, w.ok, w.tiles1, w.counts, hook > 0 ? static_cast<unsigned long long>(hook) : kWaitNs};
     TcArgs p2 = p;
     p2.tiles = w.tiles2, p2.n_tiles = w.counts + 1;
     CUtensorMap map;

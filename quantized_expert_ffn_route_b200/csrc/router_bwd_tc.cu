@@ -36,7 +36,6 @@ constexpr uint32_t kRA = kRM * kRK * 2, kRStage = kRA + kRN * kRK * 2;
 constexpr uint32_t kROffBar = kRStages * kRStage;
 constexpr uint32_t kRSmem = kROffBar + 24 * 8 + 16 + 1024;
 static_assert(2 * kRStages + 2 * kRAcc + 1 <= 24 && kRAcc * kRN <= 512, "barriers and TMEM columns");
-constexpr long kRSpin = 1L << 22;
 constexpr int kBiasRows = 64;                      // rows of dl a block sums at least
 
 struct RouterArgs {
@@ -49,7 +48,7 @@ struct RouterArgs {
     int units_w, units;                            // dW's units come first: they are the longer ones
     int bias_parts;
     unsigned *err;
-    long spin;
+    unsigned long long limit_ns;                   // of a pipeline wait
 };
 
 struct Unit {
@@ -115,8 +114,7 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
     const uint32_t tmem = *tmem_slot;
     const int bid = blockIdx.x, grid = gridDim.x;
     auto wait = [&](uint64_t *bar, uint32_t parity) {         // bounded; the same answer on every lane
-        bool ok = mbar_try_wait(bar, parity);
-        for (long i = 0; i < a.spin && !ok && !abort_s; ++i) ok = mbar_try_wait(bar, parity);
+        const bool ok = mbar_wait_ns(bar, parity, a.limit_ns, &abort_s);
         if (!ok && !abort_s) {
             report(a.err, MOE_DEVERR_TIMEOUT);
             abort_s = 1;
@@ -154,7 +152,7 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
         }
         // no copy is in flight when the block leaves, also when another role gave up
         for (int f = max(0, issued - kRStages); f < issued; ++f)
-            for (long x = 0; x < kRSpin && !mbar_try_wait(full + f % kRStages, (f / kRStages) & 1); ++x) {}
+            (void)mbar_wait_ns(full + f % kRStages, (f / kRStages) & 1, kWaitNs, nullptr);
         __syncwarp();
     } else if (warp == 1) {
         // -------------------------------------------------------------- MMA
@@ -181,9 +179,7 @@ __global__ void __launch_bounds__(kRThreads, 1) k_router_bwd(const RouterArgs a,
             mma_commit_on(on, accF + i % kRAcc);
         }
         mma_commit_on(on, drain);
-        bool done = false;
-        for (long x = 0; x < kRSpin && !done; ++x) done = mbar_try_wait(drain, 0);
-        if (!done) report(a.err, MOE_DEVERR_TIMEOUT);
+        if (!mbar_wait_ns(drain, 0, kWaitNs, nullptr)) report(a.err, MOE_DEVERR_TIMEOUT);
         __syncwarp();
     } else {
         // --------------------------------------------------------- epilogue
@@ -358,8 +354,8 @@ int launch_router_backward_tc(const RouterBackward &b, void *ws, cudaStream_t s)
     a.units_w = b.d_w ? p.mt * p.et * p.splits : 0;
     a.units = a.units_w + (b.dx ? p.mt * ((b.T + kRN - 1) / kRN) : 0);
     a.err = b.err;
-    const long hook = static_cast<long>(test_hook_value(MOE_HOOK_GEMM_SPIN));
-    a.spin = hook > 0 ? hook : kRSpin;
+    const long long hook = test_hook_value(MOE_HOOK_WAIT_LIMIT_NS);
+    a.limit_ns = hook > 0 ? static_cast<unsigned long long>(hook) : kWaitNs;
     const uint64_t hb = static_cast<uint64_t>(b.H) * 2, eb = static_cast<uint64_t>(b.E) * 2;
     CUtensorMap mw = {}, mx = {}, mk = {}, mm = {};
     int rc = MOE_OK;

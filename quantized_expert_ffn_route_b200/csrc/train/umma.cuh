@@ -33,6 +33,23 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// A wait for the phase of the given parity with a limit in time: true once it
+// has completed, false after limit_ns, or as soon as *stop is set.  The thread
+// sleeps in the hardware's wait, which is longer than a limit below 20 us (a
+// test's): with such a limit a phase that has not completed counts as late.
+constexpr unsigned long long kWaitNs = 1000000000ull;        // the limit where no test sets one
+__device__ __forceinline__ bool mbar_wait_ns(uint64_t *bar, uint32_t parity, unsigned long long limit_ns,
+                                             const volatile int *stop) {
+    if (mbar_test_wait(bar, parity)) return true;
+    if (limit_ns < 20000ull) return false;
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+    } while (!(stop && *stop) && globaltimer_ns() - t0 < limit_ns);
+    return false;
+}
+
 // One lane of the warp, the same one every time: 1 on it, 0 on the others.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t on;

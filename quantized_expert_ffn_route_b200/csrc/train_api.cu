@@ -94,11 +94,8 @@ int moe_route_backward(const float *logits, const int32_t *topk_ids, const float
 }
 
 // ---------------------------------------------------------------- experts
-// Measured at 2048 x 512, us (GEMV : GEMM): 512 experts top-10, 4 tokens 92 :
-// 115, 8 tokens 172 : 188, 16 tokens 297 : 259; 64 experts top-4, 4 tokens 48 :
-// 60, 8 tokens 76 : 64.
 static int backward_mode(int mode, int T) {
-    if (mode == MOE_MODE_AUTO) return T <= 6 ? MOE_MODE_GEMV : MOE_MODE_GEMM;
+    if (mode == MOE_MODE_AUTO) return T <= 4 ? MOE_MODE_GEMV : MOE_MODE_GEMM;
     return mode;
 }
 

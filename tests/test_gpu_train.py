@@ -406,6 +406,81 @@ def test_expert_backward_auto_mode_and_other_stream():
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
+@pytest.mark.parametrize("mode", MODES)
+def test_expert_backward_many_experts(mode):
+    """More experts than one block lists at a time, most of them without tokens."""
+    c = _Case(2, 150, 4, 128, 128, 700, True, 25)
+    dx, dw = c.run(BF16, BF16, BF16, mode)
+    assert M.moe_device_error() == 0
+    c.check(dx, dw, BF16, mode)
+
+
+@pytest.mark.parametrize("T", [0, 2, 33])
+def test_expert_backward_inconsistent_lists_stay_in_bounds(T):
+    """An `active` list that names an expert many times over, or offsets that
+    overlap: nothing is written outside the buffers, and it is reported."""
+    T = max(T, 20)
+    c = _Case(4, T, 2, 128, 128, 64, True, 26)
+    off, act, src, dst = c.perm
+    n = int(act[0])
+    twice = act.clone()
+    twice[1:1 + n] = act[1]
+    wide = off.clone()
+    wide[:64] = 0
+    wide[1:] = T * 2
+    for mode in MODES:
+        c.perm = (wide, twice, src, dst)
+        c.run(F32, F32, F32, mode)                         # checks its guard values
+        bits = M.moe_device_error()
+        if mode == M.MOE_MODE_GEMM:
+            assert bits == M.DEVERR_BAD_ROW
+    c.perm = (off, act, src, dst)
+    dx, dw = c.run(F32, F32, F32, M.MOE_MODE_GEMM)
+    c.check(dx, dw, F32, M.MOE_MODE_GEMM)
+
+
+def test_expert_backward_offsets_beyond_32_bits():
+    """Rows x hidden above 2^31: sampled tokens against the definition."""
+    T, k, H, I, E = (1 << 17) + 9, 8, 2048, 128, 8
+    assert T * (k + 1) * H > 1 << 31
+    g = np.random.Generator(np.random.PCG64(27))
+    blobs = np.stack([W.random_expert_blob(g, 4, H, I, 0.02) for _ in range(E)])
+    layer = M.MoELayer(4, H, I, E, k, blobs, blobs[0])
+    torch.manual_seed(27)
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    dy = torch.randn(T, H, device="cuda").bfloat16()
+    ids = torch.argsort(torch.rand(T, E, device="cuda"), 1).int().contiguous()
+    w = torch.softmax(torch.randn(T, k, device="cuda"), 1)
+    off, act, src, dst = _perm(ids.cpu().numpy(), E)
+    n = M.moe_expert_ffn_backward_ws_size(4, T, k, H, I, E)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dx, dw = torch.empty(T, H, device="cuda"), torch.empty(T, k, device="cuda")
+    M.moe_expert_ffn_backward(4, layer.table, off, act, src, dst, w, x, BF16, None, dy, BF16, T, k, H, I, E,
+                              layer.shared, dx, F32, dw, 0, ws, n)
+    torch.cuda.synchronize()
+    assert M.moe_device_error() == 0
+    at = np.array([0, 1, 4095, 65536, T // 2, T - 2, T - 1])
+    pick = lambda t: t[torch.from_numpy(at).cuda()].double().cpu().numpy()      # noqa: E731
+    rx, rw, ex, ew = R.experts_backward(4, H, I, blobs, blobs[0], pick(ids).astype(int), pick(w), pick(x), pick(dy),
+                                        R.U16)
+    assert (np.abs(pick(dx) - rx) <= ex).all() and (np.abs(pick(dw) - rw) <= ew).all()
+
+
+def test_expert_backward_wait_timeout_recovers():
+    """A pipeline wait that runs out sets the error word and leaves the next call exact."""
+    c = _Case(4, 200, 2, 512, 256, 8, True, 28)
+    want = c.run(F32, F32, F32, M.MOE_MODE_GEMM)
+    M.moe_test_hook(M.MOE_HOOK_WAIT_LIMIT_NS, 1)
+    try:
+        c.run(F32, F32, F32, M.MOE_MODE_GEMM)
+        assert M.moe_device_error() & M.MOE_DEVERR_TIMEOUT
+    finally:
+        M.moe_test_hook(M.MOE_HOOK_WAIT_LIMIT_NS, 0)
+    got = c.run(F32, F32, F32, M.MOE_MODE_GEMM)
+    assert M.moe_device_error() == 0
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
 # ----------------------------------------------------------------- router
 def _router_case(T, H, E, dld, xd, wd, seed):
     rng = np.random.default_rng(seed)
@@ -467,6 +542,28 @@ def test_router_backward_in_place_and_without_tokens():
     assert (dw == 0).all() and (db == 0).all()
 
 
+def test_router_backward_wait_timeout_recovers():
+    T, H, E = 700, 512, 128
+    dl, x, w, add = _router_case(T, H, E, BF16, BF16, BF16, 6)
+    n = M.moe_router_backward_ws_size(T, H, E, BF16, BF16, BF16)
+    ws = torch.empty(max(16, n), dtype=torch.uint8, device="cuda")
+
+    def run():
+        dx, dw, db = torch.empty(T, H, device="cuda"), torch.empty_like(w), torch.empty(E, device="cuda")
+        M.moe_router_backward(dl, BF16, x, BF16, w, BF16, add, T, H, E, dx, F32, dw, db, ws, n)
+        torch.cuda.synchronize()
+        return dx, dw, db
+    want = run()
+    M.moe_test_hook(M.MOE_HOOK_WAIT_LIMIT_NS, 1)
+    try:
+        run()
+        assert M.moe_device_error() & M.MOE_DEVERR_TIMEOUT
+    finally:
+        M.moe_test_hook(M.MOE_HOOK_WAIT_LIMIT_NS, 0)
+    got = run()
+    assert M.moe_device_error() == 0 and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 # ------------------------------------------------- the calls in one step
 @pytest.mark.parametrize("wdt,T,mode", [("bf16", 5, 0), ("bf16", 150, 0), ("f32", 70, 0), ("bf16", 40, M.MOE_MODE_GEMV)])
 def test_train_step(wdt, T, mode):
@@ -498,7 +595,7 @@ def test_train_step(wdt, T, mode):
     assert np.array_equal(step.counts.cpu().numpy(), counts)
     assert np.allclose(loss.cpu().numpy(), losses, rtol=1e-5)          # the call's own test has the bound
     xv = R.act8(x)[2]
-    gemm = not (mode == M.MOE_MODE_GEMV or T <= 6)
+    gemm = not (mode == M.MOE_MODE_GEMV or T <= 4)
     dx, dw, ex, ew = R.experts_backward(4, H, I, lay.blobs, lay.shared, ids, w, xv, dy.astype(np.float64),
                                         R.U16 if gemm else 0.0)
     want_dl = dl * lgrad + R.gates(ids, w, dw, E, mask != 0)
@@ -523,10 +620,11 @@ def test_train_step(wdt, T, mode):
     assert (np.abs(out["dx"].double().cpu().numpy() - want) <= b2 + R.UBF * 1.01 * (np.abs(want) + b2)).all()
 
 
-def test_train_step_in_a_graph_and_two_in_flight():
+@pytest.mark.parametrize("T", [2, 48])
+def test_train_step_in_a_graph_and_two_in_flight(T):
     """Two steps (two layers of a model) captured together and replayed on new
     inputs give what eager calls give; each owns its buffers."""
-    H, I, E, k, T = 256, 128, 16, 2, 48
+    H, I, E, k = 256, 128, 16, 2
     layers = []
     for s in (1, 2):
         lay = W.make_layer(s, 4, H, I, E, k, shared=True, w_dtype="bf16")
@@ -559,6 +657,31 @@ def test_train_step_in_a_graph_and_two_in_flight():
         for a, b in zip(outs, run(steps())):
             assert torch.equal(a, b) and torch.isfinite(a.float()).all()
     assert M.moe_device_error() == 0
+
+
+def test_steps_on_two_streams_at_once():
+    """Two steps with their own buffers, enqueued on two streams without a wait between them."""
+    H, I, E, k, T = 256, 128, 16, 2, 300
+    lay = W.make_layer(5, 4, H, I, E, k, shared=True, w_dtype="bf16")
+    g = M.MoELayer(4, H, I, E, k, lay.blobs, lay.shared, lay.w_router, "bf16")
+    steps = [M.TrainStep(g, T, BF16, balance_coef=0.1) for _ in range(2)]
+    xs = [torch.randn(T, H, device="cuda").bfloat16() for _ in range(2)]
+    dys = [torch.randn(T, H, device="cuda") for _ in range(2)]
+    want = []
+    for st, x, dy in zip(steps, xs, dys):
+        st.forward(x)
+        want.append([v.clone() for v in st.backward(dy).values()])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for st, x, dy, s in zip(steps, xs, dys, streams):
+            st.forward(x, stream=s)
+            st.backward(dy, stream=s)
+    torch.cuda.synchronize()
+    assert M.moe_device_error() == 0
+    for st, w in zip(steps, want):
+        got = [st.dx, st.d_w_router, st.d_bias]
+        assert all(torch.equal(a, b) for a, b in zip(got, w))
 
 
 def test_wrappers_refuse_wrong_tensors():
