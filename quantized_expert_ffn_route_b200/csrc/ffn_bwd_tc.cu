@@ -21,10 +21,14 @@
 // phase 2 takes its N side MN-major as it takes the weights.
 //
 // One persistent block per SM.  Roles:
-//   dequantising warps, two groups that take alternate stages, read codes
-//       straight to registers one or two of their stages ahead (no shared memory is
-//       spent on codes) and write fp16 tiles to the A stages, four blocks of 32
-//       a thread between two barriers;
+//   dequantising warps, two groups that take alternate stages, write fp16 tiles
+//       to the A stages, four blocks of 32 a thread between two barriers; the
+//       codes come by TMA to a ring of raw tiles in phase 1 (loaded by the
+//       threads, the 32-byte pieces of a K-major tile's rows kept the load unit
+//       busy: 208 of 1047 us at 8192 tokens, 148 of 396 at 64), in phase 2,
+//       whose rows are longer, straight to registers two stages ahead;
+//   one warp of phase 1 issues those copies, through a map per expert and
+//       matrix that the kernel in front makes from the blob's address;
 //   loader warps fill the B stages: phase 1 gathers the tokens' rows with
 //       cp.async (TMA's four-row gathers took 50 cycles each here: 1842 us at
 //       8192 tokens), phase 2 one warp with TMA boxes of 128 K rows x 64 tokens;
@@ -53,7 +57,8 @@ struct __align__(16) TokTile {
     int row0;      // first permuted row of the group, or -1 for the shared expert
     int n0, n;
     int at;        // column of gu16 of the first row
-    int pad[2];
+    int g;         // the group's number
+    int pad;
 };
 
 struct TcArgs {
@@ -65,6 +70,7 @@ struct TcArgs {
     float *dwp;                   // [T*k, I/32]
     float *dxp;                   // [T*k + T, H]
     uint8_t *ok;                  // [T*k]
+    const CUtensorMap *maps;      // [groups, 3]: Wg, Wu, Wd as bytes
     const TokTile *tiles;         // this phase's token tiles
     const int *n_tiles;
     unsigned long long limit_ns;  // of a pipeline wait
@@ -84,21 +90,25 @@ struct Cfg {
     static constexpr int GROUP = PHASE == 1 ? 6 : 4;          // warps of a dequantising group: 4 blocks a thread
     static constexpr int DEQ = 2 * GROUP;
     static constexpr int EPI = 4;
-    static constexpr int LOAD = PHASE == 2 ? 1 : MAXN > 64 ? 5 : 3;      // loader warps
-    static constexpr int THREADS = 32 * (DEQ + EPI + 1 + LOAD);
+    static constexpr int LOAD = PHASE == 2 ? 1 : MAXN > 64 ? 5 : 2;      // loader warps
+    static constexpr int RAW = PHASE == 1 ? 1 : 0;            // the warp that copies codes
+    static constexpr int THREADS = 32 * (DEQ + EPI + 1 + LOAD + RAW);
     static constexpr uint32_t A_STAGE = NM * kMat;
     static constexpr uint32_t B_TILE = MAXN * 128;
     static constexpr uint32_t B_STAGE = NB * B_TILE;
     static constexpr int SA = PHASE == 1 ? (MAXN > 64 ? 2 : 3) : (MAXN > 64 ? 3 : 4);
-    static constexpr int SB = PHASE == 1 ? (MAXN > 64 ? 3 : 4) : (MAXN > 64 ? 2 : 4);
+    static constexpr int SB = PHASE == 1 ? 2 : (MAXN > 64 ? 2 : 4);
+    static constexpr int SR = PHASE == 1 ? 3 : 1;             // raw code slots, a stage each (phase 2: unused)
+    static constexpr uint32_t RAW_TILE = kBM * kBK * BITS / 8, RAW_SLOT = 3 * RAW_TILE;
     static constexpr int ACC = 2 * ND * MAXN <= 512 ? 2 : 1;  // accumulator sets
     static constexpr int TMEM = ACC * ND * MAXN <= 128 ? 128 : ACC * ND * MAXN <= 256 ? 256 : 512;
     static constexpr uint32_t OFF_B = SA * A_STAGE;
-    static constexpr uint32_t OFF_SX = OFF_B + SB * B_STAGE;
+    static constexpr uint32_t OFF_RAW = OFF_B + SB * B_STAGE;
+    static constexpr uint32_t OFF_SX = OFF_RAW + (PHASE == 1 ? SR * RAW_SLOT : 0);
     static constexpr uint32_t OFF_BAR = OFF_SX + (PHASE == 1 ? EPI * MAXN * 4 : 0);   // a copy per epilogue warp
     static constexpr uint32_t SMEM = OFF_BAR + 24 * 8 + 16 + 1024;
     static_assert(SMEM <= kSmemMax, "shared memory per block");
-    static_assert(2 * SA + 2 * SB + 5 <= 24, "barrier slots");
+    static_assert(2 * SA + 2 * SB + 2 * SR + 5 <= 24, "barrier slots");
     static_assert(ACC * ND * MAXN <= 512, "TMEM columns");
     static_assert(MAXN % 16 == 0 && MAXN <= 256 && (PHASE == 1 || MAXN % 64 == 0), "tokens a tile");
 };
@@ -130,6 +140,20 @@ __device__ __forceinline__ int block_order(int p) {
 __device__ __forceinline__ int block_place(int bits, int f) {
     if (bits == 4) return f < 4 ? 8 * f : 8 * (f - 4) + 4;
     return 8 * (2 * (f & 1) + (f >> 2)) + 4 * ((f >> 1) & 1);
+}
+
+// The same from a raw tile in shared memory.
+template <int BITS>
+__device__ __forceinline__ Codes<BITS> raw_codes(const uint8_t *p) {
+    Codes<BITS> c;
+    if constexpr (BITS == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        c.w[0] = v.x, c.w[1] = v.y, c.w[2] = v.z, c.w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        c.w[0] = v.x, c.w[1] = v.y;
+    }
+    return c;
 }
 
 // Two codes at bit SHIFT of w's halves, as fp16 weights: 1024 + 2^SHIFT q from
@@ -192,6 +216,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *fullA = bars, *emptyA = bars + SA, *fullB = bars + 2 * SA, *emptyB = bars + 2 * SA + SB;
     uint64_t *accF = bars + 2 * SA + 2 * SB, *accE = accF + 2, *drain = accF + 4;
+    uint64_t *fullR = drain + 1, *emptyR = fullR + C::SR;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 24);
     volatile int &abort_s = *(reinterpret_cast<int *>(bars + 24) + 1);
     const FfnBackward &a = p.a;
@@ -212,6 +237,10 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         for (int i = 0; i < 2; ++i) {
             mbar_init(accF + i, 1);
             mbar_init(accE + i, C::EPI);
+        }
+        for (int i = 0; i < C::SR; ++i) {
+            mbar_init(fullR + i, 1);
+            mbar_init(emptyR + i, C::GROUP);
         }
         mbar_init(drain, 1);
         fence_barrier_init();
@@ -261,7 +290,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         const unsigned short *sp = nullptr;
         const int rowb = (PHASE == 1 && trans ? I : H) * BITS / 8, rows = (PHASE == 1 && trans ? I : H) / 32;
         const int cs = (trans ? KS : 32) * rowb, ss = (trans ? KS : 32) * rows;
-        const int cstep = trans ? 2 * kBK * rowb : 4 * BB, sstep = trans ? 2 * kBK * rows : 4;      // phase 1
+        const int sstep = trans ? 2 * kBK * rows : 4;         // phase 1
         int st = nk, next = 0, m0 = 0;                        // the next stage, the tile after this one
         BlobView bv = {};
         auto fetch = [&](Step<BITS> &o) {
@@ -278,16 +307,16 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
                 const __half *steps = PHASE == 2 ? (up ? bv.su : bv.sg) : mat == 0 ? bv.sg : mat == 1 ? bv.su : bv.sd;
                 const size_t row = trans ? st * C::KSTAGE - (up ? I : 0) + r : m0 + block_order<BITS>(r);
                 const int col = trans ? m0 / 32 + b : 2 * group + b;
-                cp = codes + row * rowb + col * BB;
+                if (PHASE == 2) cp = codes + row * rowb + col * BB;
                 sp = reinterpret_cast<const unsigned short *>(steps) + row * rows + col;
             }
             st += 2;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                o.c[i] = load_codes<BITS>(cp + static_cast<size_t>(i) * cs);
+                if (PHASE == 2) o.c[i] = load_codes<BITS>(cp + static_cast<size_t>(i) * cs);
                 o.s[i] = __ldg(sp + static_cast<size_t>(i) * ss);
             }
-            if (PHASE == 1) cp += cstep, sp += sstep;
+            if (PHASE == 1) sp += sstep;
         };
         // where the thread's blocks go within a stage
         const uint32_t sA = smem_addr(smem);
@@ -315,11 +344,22 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         };
         const int n = n_my * (nk / 2);
         if constexpr (PHASE == 1) {
-            // one stage ahead: the other group's stage takes longer than a load
-            // (two ahead cost registers: 1093 us against 1037 at 8192 tokens)
             Step<BITS> s0;
+            // the thread's blocks of a raw tile: as they lie in the matrix, 32 (16) or 64 (32) bytes a row
+            const uint8_t *raw = smem + C::OFF_RAW + mat * C::RAW_TILE +
+                                 (trans ? (r * 4 + b) * BB : (block_order<BITS>(r) * 2 + b) * BB);
+            const int far = trans ? KS * 4 * BB : 32 * 2 * BB;
+            int sr = group;
+            uint32_t pr = 0;
             if (n > 0) fetch(s0);
             for (int i = 0; i < n; ++i) {
+                if (!wait(fullR + sr, pr)) break;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s0.c[x] = raw_codes<BITS>(raw + sr * C::RAW_SLOT + x * far);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(emptyR + sr);
+                sr += 2;
+                if (sr >= C::SR) sr -= C::SR, pr ^= 1;
                 if (!put(s0)) break;
                 if (i + 1 < n) fetch(s0);
             }
@@ -335,12 +375,40 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
                 if (i + 3 < n) fetch(s1);
             }
         }
+    } else if (PHASE == 1 && warp == kLoad0 + C::LOAD) {
+        // ------------------------------------------------------------ codes
+        const uint32_t on = elect_one();
+        int sr = 0, issued = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int i = 0; i < n_my && ok; ++i) {
+            int m0;
+            const TokTile te = tile_of(i, m0);
+            const int y = __shfl_sync(0xffffffffu, m0, 0);
+            const CUtensorMap *maps = p.maps + 3 * static_cast<size_t>(__shfl_sync(0xffffffffu, te.g, 0));
+#pragma unroll
+            for (int m = 0; m < 3; ++m) map_acquire(maps + m);
+            for (int s = 0; s < nk; ++s) {
+                if (!(ok = wait(emptyR + sr, phase))) break;
+                const uint32_t dst = smem_addr(smem + C::OFF_RAW + sr * C::RAW_SLOT);
+                expect_tx_on(on, fullR + sr, C::RAW_SLOT);
+                tma_load_on(on, dst, maps, s * kBK * BITS / 8, y, fullR + sr);
+                tma_load_on(on, dst + C::RAW_TILE, maps + 1, s * kBK * BITS / 8, y, fullR + sr);
+                tma_load_on(on, dst + 2 * C::RAW_TILE, maps + 2, y * BITS / 8, s * kBK, fullR + sr);
+                if (++sr == C::SR) sr = 0, phase ^= 1;
+                ++issued;
+            }
+        }
+        // no copy is in flight when the block leaves, also when another role gave up
+        for (int f = max(0, issued - C::SR); f < issued; ++f)
+            (void)mbar_wait_ns(fullR + f % C::SR, (f / C::SR) & 1, kWaitNs, nullptr);
+        __syncwarp();
     } else if (PHASE == 1 && warp >= kLoad0) {
         // ------------------------------------------------- rows of x and dy
         // A warp instruction copies 128 bytes of four rows.
         const int lw = warp - kLoad0, c = lane & 7, r0 = 4 * lw + (lane >> 3);
         constexpr int RSTEP = 4 * C::LOAD, R = (MAXN + RSTEP - 1) / RSTEP;     // rows of a lane: r0 + RSTEP r
-        constexpr int D = 1;                                  // stages of copies in flight beyond the one issued
+        constexpr int D = 0;                                  // stages of copies in flight beyond the one issued
         int sb = 0, pub = 0, issued = 0;
         uint32_t phase = 1;
         bool ok = true;
@@ -573,6 +641,7 @@ struct Prep {
     int max1, max2;               // tokens per tile
     int cap1, cap2;               // entries of the lists
     int cols;                     // columns of gu16
+    CUtensorMap *maps;
 };
 
 // 2^-e and 2^e with e = floor(log2 top) of the row's largest |value| (bits
@@ -592,11 +661,13 @@ __device__ __forceinline__ int tile_rows(int n, int most) {
 }
 }  // namespace
 
-// Block 0 lists both phases' token tiles; each other block scales and rounds
-// one token's x and dy.
+// Block 0 lists both phases' token tiles, the next T blocks scale and round one
+// token's x and dy each, and the rest make the maps of the experts' codes.
 // V: float4 a thread holds of a row.
 template <int V>
-__global__ void __launch_bounds__(kPrepThreads) k_bwd_prepare(FfnBackward a, Prep p) {
+__global__ void __launch_bounds__(kPrepThreads) k_bwd_prepare(FfnBackward a, Prep p,
+                                                              const __grid_constant__ CUtensorMap rows_map,
+                                                              const __grid_constant__ CUtensorMap down_map) {
     __shared__ uint32_t part[2][kPrepThreads / 32];
     __shared__ int3 sums[kPrepThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -635,9 +706,9 @@ __global__ void __launch_bounds__(kPrepThreads) k_bwd_prepare(FfnBackward a, Pre
                 c = make_int3(0, 0, 0);
             }
             for (int i = 0; i < c.x; ++i)
-                p.tiles1[at.x + i] = {G.blob, G.row0, i * r.x, min(r.x, G.n - i * r.x), at.z + i * r.x, {0, 0}};
+                p.tiles1[at.x + i] = {G.blob, G.row0, i * r.x, min(r.x, G.n - i * r.x), at.z + i * r.x, g, 0};
             for (int i = 0; i < c.y; ++i)
-                p.tiles2[at.y + i] = {G.blob, G.row0, i * r.y, min(r.y, G.n - i * r.y), at.z + i * r.y, {0, 0}};
+                p.tiles2[at.y + i] = {G.blob, G.row0, i * r.y, min(r.y, G.n - i * r.y), at.z + i * r.y, g, 0};
         }
         pdl_next();
         const bool fits = done.x <= p.cap1 && done.y <= p.cap2 && done.z <= p.cols;
@@ -645,6 +716,20 @@ __global__ void __launch_bounds__(kPrepThreads) k_bwd_prepare(FfnBackward a, Pre
         return;
     }
     pdl_next();
+    if (static_cast<int>(blockIdx.x) > a.T) {
+        // a warp per group: the maps of its three matrices' codes
+        const int g = (static_cast<int>(blockIdx.x) - a.T - 1) * (kPrepThreads / 32) + warp;
+        const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), nullptr);
+        if (g >= n_act + (a.shared ? 1 : 0)) return;
+        const BwdGroup G = bwd_group(a, g, n_act, false);
+        if (G.n <= 0) return;
+        const BlobView bv = blob_view(G.blob, a.bits, a.H, a.I);
+        CUtensorMap *to = p.maps + 3 * static_cast<size_t>(g);
+        map_for(to, rows_map, bv.cg);
+        map_for(to + 1, rows_map, bv.cu);
+        map_for(to + 2, down_map, bv.cd);
+        return;
+    }
     const size_t t = blockIdx.x - 1;
     const int h4n = a.H / 4;
     if (tid < a.k) p.ok[t * a.k + tid] = 0;
@@ -701,6 +786,7 @@ struct TcPlan {
     int max1, max2;
     size_t tiles1, tiles2;        // bounds on the token tiles
     size_t cols;                  // and on the rows, each group's padded to 16
+    size_t groups;
 };
 constexpr int kSmallN = 64, kLargeN1 = 160, kLargeN2 = 256;
 
@@ -714,6 +800,7 @@ TcPlan plan_of(int T, int k, int E) {
     auto bound = [&](int most) { return static_cast<size_t>(rows / most + groups + T / most + 1); };
     p.tiles1 = bound(p.max1);
     p.tiles2 = bound(p.max2);
+    p.groups = static_cast<size_t>(groups + 1);
     p.cols = static_cast<size_t>((rows + T + 15 * (groups + 1) + 63) / 64 * 64);
     return p;
 }
@@ -725,6 +812,7 @@ struct TcWs {
     uint8_t *ok;
     TokTile *tiles1, *tiles2;
     int *counts;
+    CUtensorMap *maps;
 };
 
 size_t carve(int T, int k, int H, int I, int E, uint8_t *base, TcWs *out) {
@@ -747,6 +835,7 @@ size_t carve(int T, int k, int H, int I, int E, uint8_t *base, TcWs *out) {
     w.tiles1 = reinterpret_cast<TokTile *>(take(p.tiles1 * sizeof(TokTile)));
     w.tiles2 = reinterpret_cast<TokTile *>(take(p.tiles2 * sizeof(TokTile)));
     w.counts = reinterpret_cast<int *>(take(2 * sizeof(int)));
+    w.maps = reinterpret_cast<CUtensorMap *>(take(p.groups * 3 * sizeof(CUtensorMap)));
     if (out) *out = w;
     return at;
 }
@@ -781,14 +870,23 @@ int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     const TcPlan plan = plan_of(a.T, a.k, a.E);
     const Prep prep = {w.x16, w.dy16, w.scale, w.ok, w.tiles1, w.tiles2, w.counts, plan.max1, plan.max2,
                        static_cast<int>(plan.tiles1), static_cast<int>(plan.tiles2),
-                       static_cast<int>(plan.cols)};
-    if (a.H <= 2048) k_bwd_prepare<2><<<a.T + 1, kPrepThreads, 0, s>>>(a, prep);
-    else k_bwd_prepare<8><<<a.T + 1, kPrepThreads, 0, s>>>(a, prep);
+                       static_cast<int>(plan.cols), w.maps};
+    // (the base is a stand-in: each group's maps get their own)
+    CUtensorMap rows_map, down_map;
+    const uint64_t rowb = static_cast<uint64_t>(a.H) * a.bits / 8, downb = static_cast<uint64_t>(a.I) * a.bits / 8;
+    int rc = make_byte_map(&rows_map, ws, a.I, rowb, kBM, kBK * a.bits / 8);
+    if (!rc) rc = make_byte_map(&down_map, ws, a.H, downb, kBK, kBM * a.bits / 8);
+    if (rc) return rc;
+    const unsigned blocks = static_cast<unsigned>(a.T + 1 + (plan.groups + kPrepThreads / 32 - 1) / (kPrepThreads / 32));
+    if (a.H <= 2048) k_bwd_prepare<2><<<blocks, kPrepThreads, 0, s>>>(a, prep, rows_map, down_map);
+    else k_bwd_prepare<8><<<blocks, kPrepThreads, 0, s>>>(a, prep, rows_map, down_map);
     count_launches(1);
-    int rc = cuda_status(cudaGetLastError(), "backward prepare launch");
+    rc = cuda_status(cudaGetLastError(), "backward prepare launch");
     if (rc) return rc;
     const long long hook = test_hook_value(MOE_HOOK_WAIT_LIMIT_NS);
-    TcArgs p = {a, w.scale, w.gu16, static_cast<int>(plan.cols), w.x16, w.dy16, w.dwp, w.dxp, w.ok, w.tiles1, w.counts, hook > 0 ? static_cast<unsigned long long>(hook) : kWaitNs};
+    const unsigned long long limit = hook > 0 ? static_cast<unsigned long long>(hook) : kWaitNs;
+    const TcArgs p = {a, w.scale, w.gu16, static_cast<int>(plan.cols), w.x16, w.dy16, w.dwp, w.dxp, w.ok, w.maps,
+                      w.tiles1, w.counts, limit};
     TcArgs p2 = p;
     p2.tiles = w.tiles2, p2.n_tiles = w.counts + 1;
     CUtensorMap map;

@@ -44,4 +44,24 @@ int make_tensor_map(CUtensorMap *map, const void *base, int bf16, uint64_t rows,
     return MOE_OK;
 }
 
+int make_byte_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t bytes, uint32_t box_rows,
+                  uint32_t box_bytes) {
+    const EncodeTiled encode = encoder();
+    if (!encode) {
+        set_error("cuTensorMapEncodeTiled is not available in this driver");
+        return MOE_ECUDA;
+    }
+    const cuuint64_t dims[2] = {bytes, rows}, strides[1] = {bytes};
+    const cuuint32_t box[2] = {box_bytes, box_rows}, steps[2] = {1, 1};
+    const CUresult rc = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, steps,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (rc != CUDA_SUCCESS) {
+        set_error("tensor map of %llu x %llu bytes refused (CUresult %d)", static_cast<unsigned long long>(rows),
+                  static_cast<unsigned long long>(bytes), static_cast<int>(rc));
+        return MOE_ECUDA;
+    }
+    return MOE_OK;
+}
+
 }  // namespace moe

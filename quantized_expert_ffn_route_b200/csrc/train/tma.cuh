@@ -14,7 +14,31 @@ namespace moe {
 int make_tensor_map(CUtensorMap *map, const void *base, int bf16, uint64_t rows, uint64_t cols, uint64_t row_bytes,
                     uint32_t box_rows);
 
+// The same for bytes without a swizzle: boxes of box_rows x box_bytes (a
+// multiple of 16), rows one after another.
+int make_byte_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t bytes, uint32_t box_rows,
+                  uint32_t box_bytes);
+
 namespace sm100 {
+
+// A map made on the device: a copy of `like` (by one warp) for the array at
+// `base`; 128-byte aligned in global memory.  A kernel after this one may use it
+// once it has called map_acquire.
+__device__ __forceinline__ void map_for(CUtensorMap *to, const CUtensorMap &like, const void *base) {
+    const int lane = threadIdx.x & 31;
+    reinterpret_cast<uint32_t *>(to)[lane] = reinterpret_cast<const uint32_t *>(&like)[lane];
+    __syncwarp();
+    if (lane == 0)
+        asm volatile("tensormap.replace.tile.global_address.global.b1024.b64 [%0], %1;" ::"l"(
+                         __cvta_generic_to_global(to)),
+                     "l"(base)
+                     : "memory");
+    __syncwarp();
+    asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+}
+__device__ __forceinline__ void map_acquire(const CUtensorMap *map) {
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+}
 
 // A box of the map at (column x, row y) to shared memory, counted on `bar`, by
 // the lane whose `on` is 1 (the whole warp calls, with the same operands: the
