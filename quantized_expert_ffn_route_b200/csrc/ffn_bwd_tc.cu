@@ -90,15 +90,15 @@ struct Cfg {
     static constexpr int GROUP = PHASE == 1 ? 6 : 4;          // warps of a dequantising group: 4 blocks a thread
     static constexpr int DEQ = 2 * GROUP;
     static constexpr int EPI = 4;
-    static constexpr int LOAD = PHASE == 2 ? 1 : MAXN > 64 ? 5 : 2;      // loader warps
+    static constexpr int LOAD = PHASE == 2 ? 1 : MAXN > 64 ? 6 : 2;      // loader warps
     static constexpr int RAW = PHASE == 1 ? 1 : 0;            // the warp that copies codes
     static constexpr int THREADS = 32 * (DEQ + EPI + 1 + LOAD + RAW);
     static constexpr uint32_t A_STAGE = NM * kMat;
     static constexpr uint32_t B_TILE = MAXN * 128;
     static constexpr uint32_t B_STAGE = NB * B_TILE;
     static constexpr int SA = PHASE == 1 ? (MAXN > 64 ? 2 : 3) : (MAXN > 64 ? 3 : 4);
-    static constexpr int SB = PHASE == 1 ? 2 : (MAXN > 64 ? 2 : 4);
-    static constexpr int SR = PHASE == 1 ? 3 : 1;             // raw code slots, a stage each (phase 2: unused)
+    static constexpr int SB = PHASE == 1 ? (MAXN > 64 ? 3 : 2) : (MAXN > 64 ? 2 : 4);
+    static constexpr int SR = PHASE == 1 ? (MAXN > 64 ? 2 : 3) : 1;             // raw code slots, a stage each (phase 2: unused)
     static constexpr uint32_t RAW_TILE = kBM * kBK * BITS / 8, RAW_SLOT = 3 * RAW_TILE;
     static constexpr int ACC = 2 * ND * MAXN <= 512 ? 2 : 1;  // accumulator sets
     static constexpr int TMEM = ACC * ND * MAXN <= 128 ? 128 : ACC * ND * MAXN <= 256 ? 256 : 512;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         // A warp instruction copies 128 bytes of four rows.
         const int lw = warp - kLoad0, c = lane & 7, r0 = 4 * lw + (lane >> 3);
         constexpr int RSTEP = 4 * C::LOAD, R = (MAXN + RSTEP - 1) / RSTEP;     // rows of a lane: r0 + RSTEP r
-        constexpr int D = 0;                                  // stages of copies in flight beyond the one issued
+        constexpr int D = MAXN > 64 ? 1 : 0;                                  // stages of copies in flight beyond the one issued
         int sb = 0, pub = 0, issued = 0;
         uint32_t phase = 1;
         bool ok = true;
@@ -788,7 +788,7 @@ struct TcPlan {
     size_t cols;                  // and on the rows, each group's padded to 16
     size_t groups;
 };
-constexpr int kSmallN = 64, kLargeN1 = 160, kLargeN2 = 256;
+constexpr int kSmallN = 64, kLargeN1 = 128, kLargeN2 = 256;
 
 TcPlan plan_of(int T, int k, int E) {
     const long rows = static_cast<long>(T) * k, groups = rows < E ? rows : E;
