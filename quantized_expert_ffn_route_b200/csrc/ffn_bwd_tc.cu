@@ -663,8 +663,10 @@ __device__ __forceinline__ int tile_rows(int n, int most) {
 // Block 0 lists both phases' token tiles, the next T blocks scale and round one
 // token's x and dy each, and the rest make the maps of the experts' codes.
 // V: float4 a thread holds of a row.
+// V = 2 is held to seven blocks an SM, a few registers spilled: 33 us at
+// 8192 x 2048, for 48 with five blocks and none spilled.
 template <int V>
-__global__ void __launch_bounds__(kPrepThreads) k_bwd_prepare(FfnBackward a, Prep p,
+__global__ void __launch_bounds__(kPrepThreads, V <= 2 ? 7 : 1) k_bwd_prepare(FfnBackward a, Prep p,
                                                               const __grid_constant__ CUtensorMap rows_map,
                                                               const __grid_constant__ CUtensorMap down_map) {
     __shared__ uint32_t part[2][kPrepThreads / 32];
