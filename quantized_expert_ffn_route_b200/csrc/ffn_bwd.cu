@@ -11,12 +11,15 @@
 // warps are joined once at the end.  A weight is decoded exactly (code minus
 // offset is a small whole number) and once for the rows in flight.
 //
-// At one token this is a chain of memory latencies and launches: three kernels,
-// each of which may start while the one before it runs (programmatic dependent
-// launch).  (With q a pass of its own and a memset in front: 41 us at one
-// token, 512 experts, top-10; an L2 prefetch of the first codes before the wait
-// changed nothing.)  The shared expert's rows come first and split over tasks:
-// left to one task each, they were the tail at 16 tokens.
+// At one token this is a chain of memory latencies: three kernels, each of
+// which may start while the one before it runs (programmatic dependent launch).
+// 28.5 us as a graph at one token, 512 experts of 2048 x 512, top-10 (3.0 at
+// the bandwidth); with one row in flight in every task, four of its weight rows
+// loaded at once in the column sums and halves exchanged in their join, the
+// first kernel takes 12.7 us for 16.7 and the second 16.1 for 19.8.  Loads a
+// step ahead, eight at once, or three blocks an SM were slower.  The shared
+// expert's rows come first and split over tasks: left to one task each, they
+// were the tail at 16 tokens.
 #include "common.cuh"
 #include "qdot.cuh"
 #include "train/ffn_bwd.cuh"
@@ -27,7 +30,6 @@ namespace moe {
 namespace {
 constexpr int kBwThreads = 256;
 constexpr int kNT = 2;             // rows in flight
-constexpr int kLoads = 2;          // weight rows a lane has in flight in column sums
 // Column sums: columns of a task (64 of Wd, which has the fewest and the longest
 // sums, 128 of Wg and Wu).
 template <bool DOWN> struct Strip {
@@ -78,70 +80,75 @@ __device__ __forceinline__ Rows task_rows(const FfnBackward &a, int item, int n_
 }  // namespace
 
 // Pass 1, gate and up: 16 weight rows of both matrices, a warp two of each, its
-// lanes the row's chunks of 16 bytes.
+// lanes the row's chunks of 16 bytes.  The dot products of NT rows of x (xs:
+// [NT][piece][chunk]); out(row in flight, matrix, weight row, sum) on lane 0.
+template <int BITS, int NT, class Out>
+__device__ __forceinline__ void gate_up_dots(const BlobView &bv, const float4 *xs, int H, int i0, Out out) {
+    using Q = QT<BITS>;
+    const int lane = threadIdx.x & 31, nch = H / Q::EPC, nsc = H / 32;
+    const size_t rowb = static_cast<size_t>(H) * BITS / 8;
+    float dot[4][NT] = {};
+    for (int cc = lane; cc < nch; cc += 32) {
+        uint4 code[4];
+        float d[4][Q::BPC];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const size_t i = i0 + (v >> 1);
+            code[v] = ldg_stream((v & 1 ? bv.cu : bv.cg) + i * rowb + static_cast<size_t>(cc) * 16);
+            load_scales<BITS>((v & 1 ? bv.su : bv.sg) + i * nsc, cc, true, d[v]);
+        }
+#pragma unroll
+        for (int b = 0; b < Q::BPC; ++b) {
+            float acc[4][NT] = {};
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                float4 x[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) x[t] = xs[(t * Q::PPC + 8 * b + p) * nch + cc];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint32_t words[4] = {code[v].x, code[v].y, code[v].z, code[v].w};
+                    float w[4];
+                    decode4<BITS>(block_piece<BITS>(words + (BITS == 4 ? 0 : 2 * b), p), w);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        acc[v][t] = fmaf(w[3], x[t].w, fmaf(w[2], x[t].z,
+                                    fmaf(w[1], x[t].y, fmaf(w[0], x[t].x, acc[v][t]))));
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) dot[v][t] = fmaf(d[v][b], acc[v][t], dot[v][t]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float s = warp_sum(dot[v][t]);
+            if (lane == 0) out(t, v & 1, i0 + (v >> 1), s);
+        }
+}
 template <int BITS>
 __device__ __forceinline__ void gate_up(const FfnBackward &a, const GemvBwdWs &ws, const Rows &R, int rb, float4 *xs) {
-    using Q = QT<BITS>;                            // xs: [kNT][piece][chunk]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nch = a.H / Q::EPC, nsc = a.H / 32;
-    const size_t rowb = static_cast<size_t>(a.H) * BITS / 8;
+    using Q = QT<BITS>;
+    const int nch = a.H / Q::EPC, i0 = rb * 16 + (threadIdx.x >> 5) * 2;
     const BwdGroup G = R.G;
     const BlobView bv = blob_view(G.blob, BITS, a.H, a.I);
-    const int i0 = rb * 16 + warp * 2;
     const size_t out0 = G.row0 >= 0 ? G.row0 : static_cast<size_t>(a.T) * a.k;
     for (int r0 = R.r0; r0 < R.r1; r0 += kNT) {
+        const int nt = min(kNT, R.r1 - r0);
         __syncthreads();
-        for (int t = 0; t < kNT; ++t) {
-            const bool in = r0 + t < R.r1;
-            const size_t tok = in ? bwd_token(a, G, r0 + t) : 0;
+        for (int t = 0; t < nt; ++t) {
+            const size_t tok = bwd_token(a, G, r0 + t);
             for (int h4 = threadIdx.x; h4 < a.H / 4; h4 += kBwThreads)
-                xs[(t * Q::PPC + h4 % Q::PPC) * nch + h4 / Q::PPC] =
-                    in ? bwd_load4(a.x, a.x_scales, a.x_dtype, tok, a.H, h4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                xs[(t * Q::PPC + h4 % Q::PPC) * nch + h4 / Q::PPC] = bwd_load4(a.x, a.x_scales, a.x_dtype, tok, a.H, h4);
         }
         __syncthreads();
-        float dot[4][kNT] = {};
-        for (int cc = lane; cc < nch; cc += 32) {
-            uint4 code[4];
-            float d[4][Q::BPC];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const size_t i = i0 + (v >> 1);
-                code[v] = ldg_stream((v & 1 ? bv.cu : bv.cg) + i * rowb + static_cast<size_t>(cc) * 16);
-                load_scales<BITS>((v & 1 ? bv.su : bv.sg) + i * nsc, cc, true, d[v]);
-            }
-#pragma unroll
-            for (int b = 0; b < Q::BPC; ++b) {
-                float acc[4][kNT] = {};
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    float4 x[kNT];
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) x[t] = xs[(t * Q::PPC + 8 * b + p) * nch + cc];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const uint32_t words[4] = {code[v].x, code[v].y, code[v].z, code[v].w};
-                        float w[4];
-                        decode4<BITS>(block_piece<BITS>(words + (BITS == 4 ? 0 : 2 * b), p), w);
-#pragma unroll
-                        for (int t = 0; t < kNT; ++t)
-                            acc[v][t] = fmaf(w[3], x[t].w, fmaf(w[2], x[t].z,
-                                        fmaf(w[1], x[t].y, fmaf(w[0], x[t].x, acc[v][t]))));
-                    }
-                }
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) dot[v][t] = fmaf(d[v][b], acc[v][t], dot[v][t]);
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-#pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-                const float s = warp_sum(dot[v][t]);
-                if (lane == 0 && r0 + t < R.r1)
-                    ws.guq[(out0 + r0 + t) * 3 * a.I + (v & 1) * a.I + i0 + (v >> 1)] = s;
-            }
+        auto out = [&](int t, int mat, int i, float v) { ws.guq[(out0 + r0 + t) * 3 * a.I + mat * a.I + i] = v; };
+        if (nt == 1) gate_up_dots<BITS, 1>(bv, xs, a.H, i0, out);
+        else gate_up_dots<BITS, kNT>(bv, xs, a.H, i0, out);
     }
 }
 
@@ -155,6 +162,7 @@ __device__ __forceinline__ void column_sums(const BlobView &bv, const float *vs,
     const size_t rowb = static_cast<size_t>(C) * BITS / 8;
     const size_t cofs = static_cast<size_t>(col0 / 32 + blk) * 4 * BITS;
     constexpr int STEP = S::SUBS * kBwWarps;
+    constexpr int kLoads = NT == 1 ? 4 : 2;        // weight rows a lane has in flight
     for (int m0 = S::SUBS * warp + sub; m0 < M; m0 += kLoads * STEP) {
         uint32_t w[kLoads][BITS];
         float d[kLoads];
@@ -202,20 +210,26 @@ template <int BITS, bool DOWN, class Out>
 __device__ __forceinline__ void columns(const BlobView &bv, const float *vs, float *red, int nt, int M, int C, int I,
                                         int col0, Out out) {
     using S = Strip<DOWN>;                         // red: [warp][kNT][COLS]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane % S::BLOCKS, sub = lane / S::BLOCKS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blk = lane % S::BLOCKS;
     float acc[kNT][32] = {};
     if (nt == 1) column_sums<BITS, DOWN, 1>(bv, vs, M, C, I, col0, acc);
     else column_sums<BITS, DOWN, kNT>(bv, vs, M, C, I, col0, acc);
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
         if (t >= nt) break;
+        // the lanes of a block exchange halves: each step halves the columns a lane holds
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            float v = acc[t][j];
+        for (int o = 16; o >= S::BLOCKS; o >>= 1) {
+            const bool up = lane & o;
 #pragma unroll
-            for (int o = S::BLOCKS; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (sub == j % S::SUBS) red[(warp * kNT + t) * S::COLS + 32 * blk + j] = v;
+            for (int e = 0; e < o; ++e) {
+                const float give = up ? acc[t][e] : acc[t][e + o], keep = up ? acc[t][e + o] : acc[t][e];
+                acc[t][e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
         }
+#pragma unroll
+        for (int e = 0; e < S::BLOCKS; ++e)
+            red[(warp * kNT + t) * S::COLS + 32 * blk + (lane & ~(S::BLOCKS - 1)) + e] = acc[t][e];
     }
     __syncthreads();
     const int t = threadIdx.x / S::COLS, c = threadIdx.x % S::COLS;
