@@ -50,6 +50,7 @@ constexpr int kBM = 128;                    // weight rows of one product (MMA M
 constexpr int kBK = 64;                     // K per stage: 128 bytes of fp16
 constexpr uint32_t kMat = kBM * 128;        // bytes of one A tile
 constexpr size_t kSmemMax = 232448;
+constexpr int kBars = 26;                   // barrier slots
 
 // A token tile: rows n0 .. n0 + n - 1 of one group.
 struct __align__(16) TokTile {
@@ -98,7 +99,10 @@ struct Cfg {
     static constexpr uint32_t B_STAGE = NB * B_TILE;
     static constexpr int SA = PHASE == 1 ? (MAXN > 64 ? 2 : 3) : (MAXN > 64 ? 3 : 4);
     static constexpr int SB = PHASE == 1 ? (MAXN > 64 ? 3 : 2) : (MAXN > 64 ? 2 : 4);
-    static constexpr int SR = PHASE == 1 ? (MAXN > 64 ? 2 : 3) : 1;             // raw code slots, a stage each (phase 2: unused)
+    // raw code slots, a stage each (phase 2: unused); an even number, so that a
+    // slot is always the same group's: a group may be a stage ahead of the other,
+    // and the parity it waits for would tell it that the other's stage is its own
+    static constexpr int SR = 2;
     static constexpr uint32_t RAW_TILE = kBM * kBK * BITS / 8, RAW_SLOT = 3 * RAW_TILE;
     static constexpr int ACC = 2 * ND * MAXN <= 512 ? 2 : 1;  // accumulator sets
     static constexpr int TMEM = ACC * ND * MAXN <= 128 ? 128 : ACC * ND * MAXN <= 256 ? 256 : 512;
@@ -106,9 +110,10 @@ struct Cfg {
     static constexpr uint32_t OFF_RAW = OFF_B + SB * B_STAGE;
     static constexpr uint32_t OFF_SX = OFF_RAW + (PHASE == 1 ? SR * RAW_SLOT : 0);
     static constexpr uint32_t OFF_BAR = OFF_SX + (PHASE == 1 ? EPI * MAXN * 4 : 0);   // a copy per epilogue warp
-    static constexpr uint32_t SMEM = OFF_BAR + 24 * 8 + 16 + 1024;
+    static constexpr uint32_t SMEM = OFF_BAR + kBars * 8 + 16 + 1024;
     static_assert(SMEM <= kSmemMax, "shared memory per block");
-    static_assert(2 * SA + 2 * SB + 2 * SR + 5 <= 24, "barrier slots");
+    static_assert(2 * SA + 2 * SB + 2 * SR + 5 <= kBars, "barrier slots");
+    static_assert(SR % 2 == 0, "raw slots of a group");
     static_assert(ACC * ND * MAXN <= 512, "TMEM columns");
     static_assert(MAXN % 16 == 0 && MAXN <= 256 && (PHASE == 1 || MAXN % 64 == 0), "tokens a tile");
 };
@@ -217,8 +222,8 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
     uint64_t *fullA = bars, *emptyA = bars + SA, *fullB = bars + 2 * SA, *emptyB = bars + 2 * SA + SB;
     uint64_t *accF = bars + 2 * SA + 2 * SB, *accE = accF + 2, *drain = accF + 4;
     uint64_t *fullR = drain + 1, *emptyR = fullR + C::SR;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 24);
-    volatile int &abort_s = *(reinterpret_cast<int *>(bars + 24) + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
+    volatile int &abort_s = *(reinterpret_cast<int *>(bars + kBars) + 1);
     const FfnBackward &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = a.H, I = a.I;
@@ -356,6 +361,9 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
                 if (!wait(fullR + sr, pr)) break;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) s0.c[x] = raw_codes<BITS>(raw + sr * C::RAW_SLOT + x * far);
+                // the reads are done before the next copy, of the asynchronous proxy, may write here
+                // (the arrival alone does not wait for them)
+                fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(emptyR + sr);
                 sr += 2;

@@ -466,6 +466,27 @@ def test_expert_backward_offsets_beyond_32_bits():
     assert (np.abs(pick(dx) - rx) <= ex).all() and (np.abs(pick(dw) - rw) <= ew).all()
 
 
+@pytest.mark.parametrize("bits", [2, 4])
+@pytest.mark.parametrize("T,k,E", [(64, 10, 160), (700, 8, 40)])
+def test_expert_backward_with_full_pipelines(bits, T, k, E):
+    """Many long tiles a block, so that every ring of stages is in use at once:
+    the two forms agree on every row, and no run differs from another."""
+    H, I = 2048, 512
+    c = _Case(bits, T, k, H, I, E, True, 29, sigma=0.02)
+    want = c.run(M.MOE_Q8, BF16, F32, M.MOE_MODE_GEMV)
+    runs = [c.run(M.MOE_Q8, BF16, F32, M.MOE_MODE_GEMM) for _ in range(6)]
+    assert M.moe_device_error() == 0
+    # about ten roundings of half a step along a value's path, independent of each other, as in `check`
+    rms = np.sqrt(10.0) * (R.U16 + 32 * R.U32)
+    for got, ref in zip(runs[0], want):
+        off = torch.linalg.norm((got - ref).double(), dim=-1) / torch.linalg.norm(ref.double(), dim=-1)
+        assert torch.linalg.norm((got - ref).double()) <= rms * torch.linalg.norm(ref.double())
+        if got is runs[0][0]:
+            assert (off <= 2 * rms).all(), off.max()               # a row's 2048 values: within a factor of the whole's
+    for dx, dw in runs[1:]:
+        assert torch.equal(dx, runs[0][0]) and torch.equal(dw, runs[0][1])
+
+
 def test_expert_backward_wait_timeout_recovers():
     """A pipeline wait that runs out sets the error word and leaves the next call exact."""
     c = _Case(4, 200, 2, 512, 256, 8, True, 28)
