@@ -91,14 +91,14 @@ struct Cfg {
     static constexpr int GROUP = PHASE == 1 ? 6 : 4;          // warps of a dequantising group: 4 blocks a thread
     static constexpr int DEQ = 2 * GROUP;
     static constexpr int EPI = 4;
-    static constexpr int LOAD = PHASE == 2 ? 1 : MAXN > 64 ? 6 : 2;      // loader warps
+    static constexpr int LOAD = PHASE == 2 ? 1 : MAXN > 64 ? 6 : 3;      // loader warps
     static constexpr int RAW = PHASE == 1 ? 1 : 0;            // the warp that copies codes
     static constexpr int THREADS = 32 * (DEQ + EPI + 1 + LOAD + RAW);
     static constexpr uint32_t A_STAGE = NM * kMat;
     static constexpr uint32_t B_TILE = MAXN * 128;
     static constexpr uint32_t B_STAGE = NB * B_TILE;
     static constexpr int SA = PHASE == 1 ? (MAXN > 64 ? 2 : 3) : (MAXN > 64 ? 3 : 4);
-    static constexpr int SB = PHASE == 1 ? (MAXN > 64 ? 3 : 2) : (MAXN > 64 ? 2 : 4);
+    static constexpr int SB = PHASE == 1 ? 3 : (MAXN > 64 ? 2 : 4);
     // raw code slots, a stage each (phase 2: unused); an even number, so that a
     // slot is always the same group's: a group may be a stage ahead of the other,
     // and the parity it waits for would tell it that the other's stage is its own
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         // A warp instruction copies 128 bytes of four rows.
         const int lw = warp - kLoad0, c = lane & 7, r0 = 4 * lw + (lane >> 3);
         constexpr int RSTEP = 4 * C::LOAD, R = (MAXN + RSTEP - 1) / RSTEP;     // rows of a lane: r0 + RSTEP r
-        constexpr int D = MAXN > 64 ? 1 : 0;                                  // stages of copies in flight beyond the one issued
+        constexpr int D = 1;                                  // stages of copies in flight beyond the one issued
         int sb = 0, pub = 0, issued = 0;
         uint32_t phase = 1;
         bool ok = true;
