@@ -84,7 +84,7 @@ int moe_balance_loss(const float *logits, const int32_t *topk_ids, const uint8_t
  * no loss term.  d_loss device fp32 scalar (4-byte aligned) or NULL for 1.
  * topk_w/d_topk_w device fp32 [T,k], or both NULL: no gate term.  logits may
  * be NULL without a loss term, topk_ids without a gate term.  d_logits
- * device [T,E] out, dl_dtype MOE_F32 | MOE_BF16 (rounded once).  Rows of
+ * device [T,E] out (not logits itself), dl_dtype MOE_F32 | MOE_BF16 (rounded once).  Rows of
  * masked tokens are written as zeros and none of their inputs is read. */
 int moe_route_backward(const float *logits, const int32_t *topk_ids, const float *topk_w, const float *d_topk_w,
                        const uint8_t *token_mask, const int32_t *counts, const float *d_loss, int T, int E, int k,
@@ -132,8 +132,9 @@ int moe_expert_ffn_backward(int bits, const void *const *expert_blobs, const int
  * Any of dx, d_w, d_bias may be NULL (not computed); dx may be dx_in itself
  * when dx_dtype is MOE_F32.  With the three dtypes MOE_BF16 and E a multiple
  * of 8 the products run on the tensor cores (fp32 accumulation; d_w's sum over
- * tokens in up to one part per SM, added in order), else in fp32 on CUDA cores.  T = 0 writes zeros to d_w and d_bias.
- * H a positive multiple of 8, 1 <= E <= 32768.  ws: at least
+ * tokens in up to one part per SM, added in order), else in fp32 on CUDA cores.
+ * T = 0 writes zeros to d_w and d_bias.
+ * T <= 2^30, H a positive multiple of 8, 1 <= E <= 32768.  ws: at least
  * moe_router_backward_ws_size(...) bytes (may be 0: then ws may be NULL). */
 size_t moe_router_backward_ws_size(int T, int H, int E, int dl_dtype, int x_dtype, int w_dtype);
 int moe_router_backward(const void *d_logits, int dl_dtype, const void *x, int x_dtype, const void *w_router,

@@ -19,6 +19,7 @@ int moe_act_pack8(const void *x, int x_dtype, int T, int H, int8_t *codes, uint8
     REQUIRE(float_dtype(x_dtype), "x_dtype must be MOE_F32 or MOE_BF16");
     if (T == 0) return MOE_OK;
     REQUIRE(x && codes && scales, "x/codes/scales must not be NULL");
+    REQUIRE(x != static_cast<const void *>(codes), "x and codes must not be the same buffer");
     REQUIRE(aligned16(x) && aligned16(codes) && aligned16(scales), "x/codes/scales must be 16-byte aligned");
     return launch_act_pack8(x, x_dtype, static_cast<size_t>(T) * H, codes, scales, reinterpret_cast<cudaStream_t>(s));
 }
@@ -31,6 +32,7 @@ int moe_act_unpack8(const int8_t *codes, const uint8_t *scales, int T, int H, vo
     REQUIRE(float_dtype(x_dtype), "x_dtype must be MOE_F32 or MOE_BF16");
     if (T == 0) return MOE_OK;
     REQUIRE(x && codes && scales, "x/codes/scales must not be NULL");
+    REQUIRE(x != static_cast<const void *>(codes), "x and codes must not be the same buffer");
     REQUIRE(aligned16(x) && aligned16(codes) && aligned16(scales), "x/codes/scales must be 16-byte aligned");
     return launch_act_unpack8(codes, scales, static_cast<size_t>(T) * H, x, x_dtype, reinterpret_cast<cudaStream_t>(s));
 }
@@ -80,6 +82,7 @@ int moe_route_backward(const float *logits, const int32_t *topk_ids, const float
     if (T == 0) return MOE_OK;
     REQUIRE(d_logits && aligned16(d_logits), "d_logits must be given and 16-byte aligned");
     REQUIRE((topk_w != nullptr) == (d_topk_w != nullptr), "topk_w and d_topk_w go together (both or neither)");
+    REQUIRE(d_logits != static_cast<const void *>(logits), "d_logits must not be logits");
     REQUIRE(!counts || logits, "logits is NULL while counts asks for the loss's gradient");
     REQUIRE(!d_topk_w || topk_ids, "topk_ids is NULL while d_topk_w is given");
     REQUIRE((!logits || aligned16(logits)) && (!topk_ids || aligned16(topk_ids)) && (!topk_w || aligned16(topk_w)) &&
@@ -167,6 +170,7 @@ int moe_router_backward(const void *d_logits, int dl_dtype, const void *x, int x
     moe::NvtxRange nvtx_range("moe_router_backward");
     set_error("%s", "");
     REQUIRE(T >= 0, "T must be >= 0 (got %d)", T);
+    REQUIRE(T <= (1 << 30), "T too large (got %d)", T);
     REQUIRE(E >= 1 && E <= 32768, "E must be in [1, 32768] (got %d)", E);
     REQUIRE(H >= 8 && H % 8 == 0, "H must be a positive multiple of 8 (got %d)", H);
     REQUIRE(float_dtype(dl_dtype) && float_dtype(x_dtype) && float_dtype(w_dtype) && float_dtype(dx_dtype),
@@ -180,6 +184,8 @@ int moe_router_backward(const void *d_logits, int dl_dtype, const void *x, int x
             "d_logits/x/w_router/dx_in/dx/d_w/d_bias must be 16-byte aligned");
     REQUIRE(!dx || dx != static_cast<const void *>(dx_in) || dx_dtype == MOE_F32, "dx may be dx_in only in MOE_F32");
     REQUIRE(!dx || (dx != d_logits && dx != x && dx != w_router), "dx must not be d_logits, x or w_router");
+    REQUIRE(!d_w || (d_w != d_logits && d_w != x && d_w != w_router && d_w != dx && d_w != static_cast<const void *>(dx_in)),
+            "d_w must not be d_logits, x, w_router, dx_in or dx");
     const size_t need = moe_router_backward_ws_size(T, H, E, dl_dtype, x_dtype, w_dtype);
     REQUIRE(need == 0 || (ws && ws_bytes >= need && aligned16(ws)), "workspace too small: need %zu bytes", need);
     unsigned *err = device_error_word();

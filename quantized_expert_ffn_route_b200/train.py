@@ -248,8 +248,10 @@ class TrainStep:
         be finite, since they go through the layer like the others.  Returns
         (y, loss): y fp32 [T, H], loss fp32 [4] = total, balance, z, counted
         tokens."""
+        import torch
         L, T, b = self.layer, self.T, self.bufs
-        L.forward(x, self.x_dtype, T=T, mode=self.mode, stream=stream, bufs=b)
+        with torch.cuda.device(L.arena.device):        # the forward calls run on the current device
+            L.forward(x, self.x_dtype, T=T, mode=self.mode, stream=stream, bufs=b)
         moe_act_pack8(x, self.x_dtype, T, L.H, self.codes, self.scales, stream)
         self.mask = token_mask
         if self.balance_coef or self.z_coef:

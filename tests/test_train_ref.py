@@ -115,10 +115,12 @@ def _refused(name, args, changes):
 def test_act8_refusals():
     _, p = _buf()
     bad = [{1: 7}, {1: M.MOE_Q8}, {2: -1}, {3: 0}, {3: 48}, {0: None}, {4: None}, {5: None}, {0: p + 8}, {4: p + 4},
-           {5: p + 1}]
-    _refused("moe_act_pack8", [p, 0, 4, 64, p, p, None], bad)
-    _refused("moe_act_unpack8", [p, p, 4, 64, p, 0, None],
-             [{5: 7}, {5: 2}, {2: -1}, {3: 16}, {0: None}, {1: None}, {4: None}, {0: p + 8}, {1: p + 8}, {4: p + 8}])
+           {5: p + 1}, {4: p}]
+    q = p + 4096
+    _refused("moe_act_pack8", [p, 0, 4, 64, q, q, None], bad)
+    _refused("moe_act_unpack8", [q, q, 4, 64, p, 0, None],
+             [{5: 7}, {5: 2}, {2: -1}, {3: 16}, {0: None}, {1: None}, {4: None}, {0: p + 8}, {1: p + 8}, {4: p + 8},
+              {0: p}])
     assert M.lib().moe_act_pack8(None, 0, 0, 64, None, None, None) == M.MOE_OK
     assert M.lib().moe_act_unpack8(None, None, 0, 64, None, 1, None) == M.MOE_OK
 
@@ -131,10 +133,10 @@ def test_balance_refusals():
     _refused("moe_balance_loss", good,
              [{3: -1}, {4: 0}, {4: 32769}, {5: 0}, {5: 17}, {5: 33, 4: 64}, {3: 1 << 30, 5: 2}, {0: None}, {1: None},
               {8: None}, {9: None}, {10: None}, {11: n - 1}, {0: p + 4}, {1: p + 4}, {8: p + 4}, {9: p + 4}, {10: p + 8}])
-    good = [p, p, p, p, None, p, None, 4, 16, 2, 1.0, 0.0, p, 0, None]
+    good = [p, p, p, p, None, p, None, 4, 16, 2, 1.0, 0.0, p + 4096, 0, None]
     _refused("moe_route_backward", good,
              [{7: -1}, {8: 0}, {9: 0}, {9: 17}, {13: 2}, {13: -1}, {12: None}, {12: p + 4}, {2: None}, {3: None},
-              {0: None}, {1: None}, {0: p + 4}, {2: p + 4}, {3: p + 8}, {5: p + 4}, {6: p + 2}])
+              {0: None}, {1: None}, {0: p + 4}, {2: p + 4}, {3: p + 8}, {5: p + 4}, {6: p + 2}, {12: p}])
     assert M.lib().moe_route_backward(*([None] * 7), 0, 16, 2, 1.0, 0.0, None, 0, None) == M.MOE_OK
 
 
@@ -162,10 +164,11 @@ def test_router_backward_refusals():
     T, H, E = 4, 64, 16
     q, r = p + 4096, p + 8192
     #       dl dld x xd w wd dx_in T H E dx dxd dw db ws n
-    good = [p, 0, p, 0, p, 0, None, T, H, E, q, 0, p, p, None, 0, None]
+    good = [p, 0, p, 0, p, 0, None, T, H, E, q, 0, r, r, None, 0, None]
     _refused("moe_router_backward", good,
              [{1: 2}, {3: 2}, {5: 7}, {11: 2}, {7: -1}, {8: 0}, {8: 12}, {9: 0}, {9: 32769}, {0: None}, {2: None},
-              {4: None}, {10: None, 12: None, 13: None}, {10: p}, {6: q, 11: 1}] +
+              {4: None}, {10: None, 12: None, 13: None}, {10: p}, {6: q, 11: 1}, {12: p},
+              {12: q}, {6: r}, {7: (1 << 30) + 1}] +
              [{i: p + 8} for i in (0, 2, 4, 6, 10, 12, 13)])
     # large bf16 products need the workspace that the size call asks for
     n = M.moe_router_backward_ws_size(8192, 2048, 512, 1, 1, 1)
