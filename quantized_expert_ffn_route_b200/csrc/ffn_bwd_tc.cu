@@ -22,11 +22,13 @@
 //
 // One persistent block per SM.  Roles:
 //   dequantising warps, two groups that take alternate stages, write fp16 tiles
-//       to the A stages, four blocks of 32 a thread between two barriers; the
-//       codes come by TMA to a ring of raw tiles in phase 1 (loaded by the
-//       threads, the 32-byte pieces of a K-major tile's rows kept the load unit
-//       busy: 208 of 1047 us at 8192 tokens, 148 of 396 at 64), in phase 2,
-//       whose rows are longer, straight to registers two stages ahead;
+//       to the A stages, four blocks of 32 a thread between two barriers.  g's
+//       and u's A tiles go to TMEM, a row a lane (848 us for 775 at 8192 tokens:
+//       in shared memory they were half of its traffic); transposed tiles lie in
+//       shared memory.  The codes come by TMA to a ring of raw tiles in phase 1
+//       (loaded by the threads, the 32-byte pieces of a K-major tile's rows kept
+//       the load unit busy: 208 of 1047 us at 8192 tokens, 148 of 396 at 64), in
+//       phase 2, whose rows are longer, straight to registers two stages ahead;
 //   one warp of phase 1 issues those copies, through a map per expert and
 //       matrix that the kernel in front makes from the blob's address;
 //   loader warps fill the B stages: phase 1 gathers the tokens' rows with
@@ -38,13 +40,16 @@
 // and TMEM is freed).
 //
 // Measured (512 experts of 2048 x 512 and a shared one, top-10, 4 bits, 8192
-// tokens): preparation 33 us, phase 1 845, phase 2 522, gather 141; 945 GFLOP at
-// 613 TFLOP/s.  No role alone bounds the two phases: of phase 1's then 947 us,
-// copying no rows saves 37, dequantising nothing 64, the epilogue's work 200, all
-// three 382; of phase 2's 527, its stores 78, its codes 55, its B copies 55, its
-// MMAs 65.  A tile of 128 rows (phase 1) leaves room for three B stages (160 rows
-// and two: 1071 us for 944); of 256 (phase 2) reads the weights least (192: 564
-// us for 526, 128: 605).  The gather moves its 770 MB at 5.5 TB/s.
+// tokens): preparation 33 us, phase 1 775, phase 2 525, gather 141; 945 GFLOP at
+// 640 TFLOP/s.  No role alone bounds the two phases: of phase 1's, copying no rows
+// saves 27, writing no transposed tiles 37, the epilogue's work 120, the MMAs 34;
+// of phase 2's, its stores 78, its codes 55, its B copies 55, its MMAs 65.  A tile
+// of 128 rows (phase 1) leaves room for three B stages and fills TMEM with its
+// accumulators and A (96 rows and three A stages: 862 us); of 256 (phase 2) reads
+// the weights least (192: 564 us for 526, 128: 605).  The gather moves its 770 MB
+// at 5.5 TB/s.  At 16 tokens (phases 103 and 72) the transposed tile's warps take
+// longest; twice as many of them gained 4 us there and cost 80 at 8192, in
+// registers.
 #include "common.cuh"
 #include "kernels.h"
 #include "train/ffn_bwd.cuh"
@@ -60,7 +65,7 @@ constexpr int kBM = 128;                    // weight rows of one product (MMA M
 constexpr int kBK = 64;                     // K per stage: 128 bytes of fp16
 constexpr uint32_t kMat = kBM * 128;        // bytes of one A tile
 constexpr size_t kSmemMax = 232448;
-constexpr int kBars = 26;                   // barrier slots
+constexpr int kBars = 28;                   // barrier slots
 
 // A token tile: rows n0 .. n0 + n - 1 of one group.
 struct __align__(16) TokTile {
@@ -104,18 +109,21 @@ struct Cfg {
     static constexpr int LOAD = PHASE == 2 ? 1 : MAXN > 64 ? 6 : 3;      // loader warps
     static constexpr int RAW = PHASE == 1 ? 1 : 0;            // the warp that copies codes
     static constexpr int THREADS = 32 * (DEQ + EPI + 1 + LOAD + RAW);
-    static constexpr uint32_t A_STAGE = NM * kMat;
+    // phase 1: g's and u's A tiles lie in TMEM, 32 columns each
+    static constexpr int NS = PHASE == 1 ? 1 : NM;            // A tiles in shared memory
+    static constexpr uint32_t A_STAGE = NS * kMat;
     static constexpr uint32_t B_TILE = MAXN * 128;
     static constexpr uint32_t B_STAGE = NB * B_TILE;
-    static constexpr int SA = PHASE == 1 ? (MAXN > 64 ? 2 : 3) : (MAXN > 64 ? 3 : 4);
+    static constexpr int SA = PHASE == 1 ? 2 : (MAXN > 64 ? 3 : 4);
     static constexpr int SB = PHASE == 1 ? 3 : (MAXN > 64 ? 2 : 4);
     // raw code slots, a stage each (phase 2: unused); an even number, so that a
     // slot is always the same group's: a group may be a stage ahead of the other,
     // and the parity it waits for would tell it that the other's stage is its own
-    static constexpr int SR = 2;
+    static constexpr int SR = PHASE == 1 && MAXN <= 64 ? 4 : 2;
     static constexpr uint32_t RAW_TILE = kBM * kBK * BITS / 8, RAW_SLOT = 3 * RAW_TILE;
-    static constexpr int ACC = 2 * ND * MAXN <= 512 ? 2 : 1;  // accumulator sets
-    static constexpr int TMEM = ACC * ND * MAXN <= 128 ? 128 : ACC * ND * MAXN <= 256 ? 256 : 512;
+    static constexpr int TA = PHASE == 1 ? 64 * SA : 0;       // TMEM columns of A
+    static constexpr int ACC = 2 * ND * MAXN + TA <= 512 ? 2 : 1;         // accumulator sets
+    static constexpr int COLS = ACC * ND * MAXN + TA, TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static constexpr uint32_t OFF_B = SA * A_STAGE;
     static constexpr uint32_t OFF_RAW = OFF_B + SB * B_STAGE;
     static constexpr uint32_t OFF_SX = OFF_RAW + (PHASE == 1 ? SR * RAW_SLOT : 0);
@@ -124,7 +132,7 @@ struct Cfg {
     static_assert(SMEM <= kSmemMax, "shared memory per block");
     static_assert(2 * SA + 2 * SB + 2 * SR + 5 <= kBars, "barrier slots");
     static_assert(SR % 2 == 0, "raw slots of a group");
-    static_assert(ACC * ND * MAXN <= 512, "TMEM columns");
+    static_assert(COLS <= 512, "TMEM columns");
     static_assert(MAXN % 16 == 0 && MAXN <= 256 && (PHASE == 1 || MAXN % 64 == 0), "tokens a tile");
 };
 
@@ -213,6 +221,29 @@ __device__ __forceinline__ void put_block(const Codes<BITS> &c, __half d, uint32
     }
 }
 
+// A block's 32 values as 16 words, in block_order.
+template <int BITS>
+__device__ __forceinline__ void block_words(const Codes<BITS> &c, __half d, uint32_t (&o)[16]) {
+    const __half2 d2 = __half2half2(d);
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = c.w[j], v = w >> 8;
+            o[4 * j] = weight2<4, 0>(w, d2), o[4 * j + 1] = weight2<4, 0>(v, d2);
+            o[4 * j + 2] = weight2<4, 4>(w, d2), o[4 * j + 3] = weight2<4, 4>(v, d2);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t w = c.w[j], v = w >> 8;
+            o[8 * j] = weight2<2, 0>(w, d2), o[8 * j + 1] = weight2<2, 0>(v, d2);
+            o[8 * j + 2] = weight2<2, 2>(w, d2), o[8 * j + 3] = weight2<2, 2>(v, d2);
+            o[8 * j + 4] = weight2<2, 4>(w, d2), o[8 * j + 5] = weight2<2, 4>(v, d2);
+            o[8 * j + 6] = weight2<2, 6>(w, d2), o[8 * j + 7] = weight2<2, 6>(v, d2);
+        }
+    }
+}
+
 // What a dequantising thread reads for one stage: four blocks and their steps.
 template <int BITS> struct Step {
     Codes<BITS> c[4];
@@ -293,19 +324,20 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         // Group 0 takes the even stages, group 1 the odd ones.
         const int group = warp / C::GROUP, t = tid - group * 32 * C::GROUP;
         constexpr int BB = 4 * BITS;                          // bytes of a block's codes
-        // phase 1: g and u: (row + 32 i, half of the stage's K); q and phase 2: (K index + KS i, block of
-        // columns).  Neighbouring lanes take the blocks of a row: whole sectors.
-        const int mat = PHASE == 1 ? t >> 6 : 0;
-        const bool trans = PHASE == 2 || mat == 2;
+        // phase 1: four warps g and u, a thread a row of the warp's TMEM lanes (its two blocks of g, then of
+        // u), two warps q; q and phase 2: (K index + KS i, block of columns), neighbouring lanes the blocks
+        // of a row.
+        const bool trans = PHASE == 2 || t >= 128;
         constexpr int KS = PHASE == 1 ? 16 : 32;
-        const int tt = PHASE == 1 ? t & 63 : t;
-        const int b = trans ? tt & 3 : tt & 1, r = trans ? tt >> 2 : tt >> 1;
+        const int tt = PHASE == 1 ? t - 128 : t, b = tt & 3, r = tt >> 2;
+        const int row_m = 32 * (warp & 3) + block_order<BITS>(lane);          // g and u: the row of the tile
         // the source of the next stage: pointers of the first block, distances of the others and of stages
         const uint8_t *cp = nullptr;
         const unsigned short *sp = nullptr;
         const int rowb = (PHASE == 1 && trans ? I : H) * BITS / 8, rows = (PHASE == 1 && trans ? I : H) / 32;
-        const int cs = (trans ? KS : 32) * rowb, ss = (trans ? KS : 32) * rows;
+        const int cs = KS * rowb, ss = KS * rows;
         const int sstep = trans ? 2 * kBK * rows : 4;         // phase 1
+        const size_t u_off = static_cast<size_t>(I) * H / 32; // from g's steps to u's
         int st = nk, next = 0, m0 = 0;                        // the next stage, the tile after this one
         BlobView bv = {};
         auto fetch = [&](Step<BITS> &o) {
@@ -318,39 +350,59 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
             if (PHASE == 2 || start) {
                 // phase 2: Wg's I / 128 stages, then Wu's
                 const bool up = PHASE == 2 && st * C::KSTAGE >= I;
-                const uint8_t *codes = PHASE == 2 ? (up ? bv.cu : bv.cg) : mat == 0 ? bv.cg : mat == 1 ? bv.cu : bv.cd;
-                const __half *steps = PHASE == 2 ? (up ? bv.su : bv.sg) : mat == 0 ? bv.sg : mat == 1 ? bv.su : bv.sd;
-                const size_t row = trans ? st * C::KSTAGE - (up ? I : 0) + r : m0 + block_order<BITS>(r);
-                const int col = trans ? m0 / 32 + b : 2 * group + b;
+                const uint8_t *codes = up ? bv.cu : bv.cg;
+                const __half *steps = PHASE == 2 ? (up ? bv.su : bv.sg) : trans ? bv.sd : bv.sg;
+                const size_t row = trans ? st * C::KSTAGE - (up ? I : 0) + r : m0 + row_m;
+                const int col = trans ? m0 / 32 + b : 2 * group;
                 if (PHASE == 2) cp = codes + row * rowb + col * BB;
                 sp = reinterpret_cast<const unsigned short *>(steps) + row * rows + col;
             }
             st += 2;
+            if (trans) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (PHASE == 2) o.c[i] = load_codes<BITS>(cp + static_cast<size_t>(i) * cs);
-                o.s[i] = __ldg(sp + static_cast<size_t>(i) * ss);
+                for (int i = 0; i < 4; ++i) {
+                    if (PHASE == 2) o.c[i] = load_codes<BITS>(cp + static_cast<size_t>(i) * cs);
+                    o.s[i] = __ldg(sp + static_cast<size_t>(i) * ss);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t two = __ldg(reinterpret_cast<const unsigned *>(sp + i * u_off));
+                    o.s[2 * i] = static_cast<unsigned short>(two), o.s[2 * i + 1] = static_cast<unsigned short>(two >> 16);
+                }
             }
             if (PHASE == 1) sp += sstep;
         };
         // where the thread's blocks go within a stage
         const uint32_t sA = smem_addr(smem);
-        const uint32_t to = trans ? mat * kMat + (b >> 1) * 8192 + r * 128 : mat * kMat + r * 128;
-        const int c0 = trans ? 4 * (b & 1) : 4 * b, sw = r & 7;
-        const bool flip = trans && b >= 2;
+        const uint32_t to = (b >> 1) * 8192 + r * 128;
+        const int c0 = 4 * (b & 1), sw = r & 7;
+        const bool flip = b >= 2;
+        const uint32_t to_t = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + C::COLS - C::TA;
         int sa = group % SA;
         uint32_t phase = 1;                                   // the first pass over the ring finds it empty
         auto put = [&](const Step<BITS> &o) {
             if (!wait(emptyA + sa, phase)) return false;
-            const uint32_t at = sA + sa * C::A_STAGE + to;
+            if (trans) {
+                const uint32_t at = sA + sa * C::A_STAGE + to;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // rows 32 i on (32 x 128 bytes); K rows KS i on: 128 bytes each, 64 rows a tile
-                const uint32_t off = PHASE == 1 ? (trans ? i * KS * 128 : i * 32 * 128)
-                                                : (i >> 1) * kMat + (i & 1) * KS * 128;
-                put_block<BITS>(o.c[i], __ushort_as_half(o.s[i]), at + off, c0, sw, flip);
+                for (int i = 0; i < 4; ++i) {
+                    // K rows KS i on: 128 bytes each, 64 rows a tile
+                    const uint32_t off = PHASE == 1 ? i * KS * 128 : (i >> 1) * kMat + (i & 1) * KS * 128;
+                    put_block<BITS>(o.c[i], __ushort_as_half(o.s[i]), at + off, c0, sw, flip);
+                }
+                fence_proxy_async();
+            } else {
+                tc_fence_after();                             // the MMAs that read the stage are done
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t words[16];
+                    block_words<BITS>(o.c[i], __ushort_as_half(o.s[i]), words);
+                    tmem_st16(to_t + sa * 64 + i * 16, words);
+                }
+                tmem_st_wait();
+                tc_fence_before();
             }
-            fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(fullA + sa);
             sa += 2;
@@ -360,17 +412,27 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         const int n = n_my * (nk / 2);
         if constexpr (PHASE == 1) {
             Step<BITS> s0;
-            // the thread's blocks of a raw tile: as they lie in the matrix, 32 (16) or 64 (32) bytes a row
-            const uint8_t *raw = smem + C::OFF_RAW + mat * C::RAW_TILE +
-                                 (trans ? (r * 4 + b) * BB : (block_order<BITS>(r) * 2 + b) * BB);
-            const int far = trans ? KS * 4 * BB : 32 * 2 * BB;
+            // the thread's blocks of the raw tiles, as they lie in the matrices: four a row of Wd's, two of
+            // the others', where half of the lanes read the second first (other banks)
+            const uint8_t *raw = smem + C::OFF_RAW + (trans ? 2 * C::RAW_TILE + (r * 4 + b) * BB : row_m * 2 * BB);
+            const bool second = lane & 4;
             int sr = group;
             uint32_t pr = 0;
             if (n > 0) fetch(s0);
             for (int i = 0; i < n; ++i) {
                 if (!wait(fullR + sr, pr)) break;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) s0.c[x] = raw_codes<BITS>(raw + sr * C::RAW_SLOT + x * far);
+                for (int x = 0; x < 4; ++x) {
+                    const int at = trans ? x * KS * 4 * BB : (x >> 1) * C::RAW_TILE + ((x & 1) ^ second) * BB;
+                    s0.c[x] = raw_codes<BITS>(raw + sr * C::RAW_SLOT + at);
+                }
+                if (!trans && second) {
+#pragma unroll
+                    for (int x = 0; x < 4; x += 2) {
+                        const Codes<BITS> c = s0.c[x];
+                        s0.c[x] = s0.c[x + 1], s0.c[x + 1] = c;
+                    }
+                }
                 // the reads are done before the next copy, of the asynchronous proxy, may write here
                 // (the arrival alone does not wait for them)
                 fence_proxy_async();
@@ -619,12 +681,16 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
 #pragma unroll
                 for (int mat = 0; mat < NM; ++mat) {
                     const bool trans = PHASE == 2 || mat == 2;
-                    const uint64_t am = as + mat * (kMat >> 4);
+                    const uint64_t am = as + (PHASE == 1 ? 0 : mat * (kMat >> 4));
                     const uint64_t bm = bs + (PHASE == 1 ? (mat == 2) * (C::B_TILE >> 4) : mat * (8192 >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        mma_f16_on(on, d + (PHASE == 1 ? mat : 0) * MAXN, trans ? mn + am + kk * 128 : km + am + kk * 2,
-                                   PHASE == 2 ? mnb + bm + kk * 128 : km + bm + kk * 2, trans ? id_mn : id_k, (PHASE == 1 ? s | kk : s | kk | mat) != 0);
+                    for (int kk = 0; kk < kBK / 16; ++kk) {
+                        const uint64_t bk = PHASE == 2 ? mnb + bm + kk * 128 : km + bm + kk * 2;
+                        const uint32_t dm = d + (PHASE == 1 ? mat : 0) * MAXN;
+                        const uint32_t more = PHASE == 1 ? s | kk : s | kk | mat;
+                        if (trans) mma_f16_on(on, dm, mn + am + kk * 128, bk, id_mn, more != 0);
+                        else mma_f16_ts_on(on, dm, tm + C::COLS - C::TA + sa * 64 + mat * 32 + kk * 8, bk, id_k, more != 0);
+                    }
                 }
                 mma_commit_on(on, emptyA + sa);
                 mma_commit_on(on, emptyB + sb);
