@@ -56,6 +56,7 @@
 #include "train/launch.cuh"
 #include "train/tma.cuh"
 #include "train/umma.cuh"
+#include "train/ws.h"
 
 namespace moe {
 using namespace sm100;
@@ -900,13 +901,15 @@ struct TcWs {
     CUtensorMap *maps;
 };
 
+// The parts of a workspace at `base` (a multiple of kWsAlign: the maps' addresses
+// need 128), each at a multiple of kWsAlign; returns their bytes.
 size_t carve(int T, int k, int H, int I, int E, uint8_t *base, TcWs *out) {
     const size_t rows = static_cast<size_t>(T) * k, all = rows + T;
     const TcPlan p = plan_of(T, k, E);
     size_t at = 0;
     auto take = [&](size_t n) {
         uint8_t *q = base ? base + at : nullptr;
-        at += (n + 255) / 256 * 256;
+        at += (n + kWsAlign - 1) / kWsAlign * kWsAlign;
         return q;
     };
     TcWs w;
@@ -939,7 +942,9 @@ int launch_phase(const TcArgs &p, const CUtensorMap &map, cudaStream_t s) {
 }
 }  // namespace
 
-size_t ffn_backward_gemm_ws_bytes(int T, int k, int H, int I, int E) { return carve(T, k, H, I, E, nullptr, nullptr); }
+size_t ffn_backward_gemm_ws_bytes(int T, int k, int H, int I, int E) {
+    return carve(T, k, H, I, E, nullptr, nullptr) + kWsSlack;
+}
 
 bool ffn_backward_gemm_supported(int T, int k, int H, int I, int E) {
     // tile and step numbers are ints
@@ -951,7 +956,7 @@ bool ffn_backward_gemm_supported(int T, int k, int H, int I, int E) {
 
 int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     TcWs w;
-    carve(a.T, a.k, a.H, a.I, a.E, static_cast<uint8_t *>(ws), &w);
+    carve(a.T, a.k, a.H, a.I, a.E, ws_start(ws), &w);
     const TcPlan plan = plan_of(a.T, a.k, a.E);
     const Prep prep = {w.x16, w.dy16, w.scale, w.ok, w.tiles1, w.tiles2, w.counts, plan.max1, plan.max2,
                        static_cast<int>(plan.tiles1), static_cast<int>(plan.tiles2),
@@ -959,8 +964,8 @@ int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     // (the base is a stand-in: each group's maps get their own)
     CUtensorMap rows_map, down_map;
     const uint64_t rowb = static_cast<uint64_t>(a.H) * a.bits / 8, downb = static_cast<uint64_t>(a.I) * a.bits / 8;
-    int rc = make_byte_map(&rows_map, ws, a.I, rowb, kBM, kBK * a.bits / 8);
-    if (!rc) rc = make_byte_map(&down_map, ws, a.H, downb, kBK, kBM * a.bits / 8);
+    int rc = make_byte_map(&rows_map, w.x16, a.I, rowb, kBM, kBK * a.bits / 8);
+    if (!rc) rc = make_byte_map(&down_map, w.x16, a.H, downb, kBK, kBM * a.bits / 8);
     if (rc) return rc;
     const unsigned blocks = static_cast<unsigned>(a.T + 1 + (plan.groups + kPrepThreads / 32 - 1) / (kPrepThreads / 32));
     if (a.H <= 2048) k_bwd_prepare<2><<<blocks, kPrepThreads, 0, s>>>(a, prep, rows_map, down_map);
