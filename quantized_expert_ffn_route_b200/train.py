@@ -247,9 +247,13 @@ class TrainStep:
         padding (kept for the backward pass), or None; rows of padding have to
         be finite, since they go through the layer like the others.  Returns
         (y, loss): y fp32 [T, H], loss fp32 [4] = total, balance, z, counted
-        tokens."""
+        tokens.  Arguments are checked before anything is launched; after an
+        error there is no backward() until a forward() has succeeded."""
         import torch
-        L, T, b = self.layer, self.T, self.bufs
+        self._ran = False                               # the buffers below belong to no whole step until the end
+        L, T, b, n = self.layer, self.T, self.bufs, "TrainStep.forward"
+        d, _ = _p(L.arena.device.index, n, "x", x, _any(self.x_dtype), T * L.H)
+        _p(d, n, "token_mask", token_mask, _T["mask"], T)
         with torch.cuda.device(L.arena.device):        # the forward calls run on the current device
             L.forward(x, self.x_dtype, T=T, mode=self.mode, stream=stream, bufs=b)
         moe_act_pack8(x, self.x_dtype, T, L.H, self.codes, self.scales, stream)
@@ -269,6 +273,8 @@ class TrainStep:
             raise RuntimeError("TrainStep.backward() needs a forward() first")
         L, T, b = self.layer, self.T, self.bufs
         E, H, I, k = L.E, L.H, L.I, L.k
+        d, _ = _p(L.arena.device.index, "TrainStep.backward", "dy", dy, _any(self.dy_dtype), T * H)
+        _p(d, "TrainStep.backward", "d_loss", d_loss, _T[0], 1)
         loss = bool(self.balance_coef or self.z_coef)
         moe_expert_ffn_backward(L.bits, L.table, b.offsets, b.active, b.perm_src, b.perm_dst, b.w, self.codes, MOE_Q8,
                                 self.scales, dy, self.dy_dtype, T, k, H, I, E, L.shared, self.dx_experts, 0,
