@@ -211,8 +211,6 @@ class TrainStep:
 
     def __init__(self, layer, T, x_dtype, dy_dtype=0, dx_dtype=None, mode=0, balance_coef=0.0, z_coef=0.0):
         import torch
-        from . import MOE_BF16
-        from .layer import alloc_step_buffers
         if layer.w_router is None:
             raise ValueError("TrainStep needs a layer with a router")
         if T < 1:
@@ -221,14 +219,25 @@ class TrainStep:
         self.x_dtype, self.dy_dtype = x_dtype, dy_dtype
         self.dx_dtype = x_dtype if dx_dtype is None else dx_dtype
         self.balance_coef, self.z_coef = float(balance_coef), float(z_coef)
-        E, H, I, k, dev = layer.E, layer.H, layer.I, layer.k, layer.device
+        self.device = layer.arena.device                # layer.device may have no index
+        with torch.cuda.device(self.device):            # sizes follow the current device
+            self._allocate()
+        self.mask = None
+        self._ran = False
+
+    def _allocate(self):
+        import torch
+        from . import MOE_BF16
+        from .layer import alloc_step_buffers
+        layer, T, mode, dev = self.layer, self.T, self.mode, self.device
+        E, H, I, k = layer.E, layer.H, layer.I, layer.k
+
         def new(n, dtype):
             return torch.empty(n, dtype=dtype, device=dev)
         f32, u8 = torch.float32, torch.uint8
         self.bufs = alloc_step_buffers(T, H, I, E, k, layer.bits, mode, dev, layer.shared is not None)
         self.codes, self.scales = new((T, H), torch.int8), new((T, H // 32), u8)
         self.counts, self.loss = new(E + 1, torch.int32), torch.zeros(4, dtype=f32, device=dev)
-        self.mask = None
         # the router's products read the checkpoint as bf16 when its weights are bf16 (exact either way)
         self.dl_dtype = self.r_dtype = layer.w_dtype
         wide = torch.bfloat16 if layer.w_dtype == MOE_BF16 else f32
@@ -240,7 +249,6 @@ class TrainStep:
                           ffn=moe_expert_ffn_backward_ws_size(layer.bits, T, k, H, I, E, mode),
                           router=moe_router_backward_ws_size(T, H, E, self.dl_dtype, self.r_dtype, layer.w_dtype))
         self.ws = new(max(16, *self.sizes.values()), u8)
-        self._ran = False
 
     def forward(self, x, token_mask=None, stream=None):
         """x: device [T, H] (x_dtype); token_mask: device uint8/bool [T], 0 for
@@ -252,9 +260,9 @@ class TrainStep:
         import torch
         self._ran = False                               # the buffers below belong to no whole step until the end
         L, T, b, n = self.layer, self.T, self.bufs, "TrainStep.forward"
-        d, _ = _p(L.arena.device.index, n, "x", x, _any(self.x_dtype), T * L.H)
+        d, _ = _p(self.device.index, n, "x", x, _any(self.x_dtype), T * L.H)
         _p(d, n, "token_mask", token_mask, _T["mask"], T)
-        with torch.cuda.device(L.arena.device):        # the forward calls run on the current device
+        with torch.cuda.device(self.device):            # the forward calls run on the current device
             L.forward(x, self.x_dtype, T=T, mode=self.mode, stream=stream, bufs=b)
         moe_act_pack8(x, self.x_dtype, T, L.H, self.codes, self.scales, stream)
         self.mask = token_mask
@@ -273,7 +281,7 @@ class TrainStep:
             raise RuntimeError("TrainStep.backward() needs a forward() first")
         L, T, b = self.layer, self.T, self.bufs
         E, H, I, k = L.E, L.H, L.I, L.k
-        d, _ = _p(L.arena.device.index, "TrainStep.backward", "dy", dy, _any(self.dy_dtype), T * H)
+        d, _ = _p(self.device.index, "TrainStep.backward", "dy", dy, _any(self.dy_dtype), T * H)
         _p(d, "TrainStep.backward", "d_loss", d_loss, _T[0], 1)
         loss = bool(self.balance_coef or self.z_coef)
         moe_expert_ffn_backward(L.bits, L.table, b.offsets, b.active, b.perm_src, b.perm_dst, b.w, self.codes, MOE_Q8,

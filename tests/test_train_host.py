@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import quantized_expert_ffn_route_b200 as M
+from quantized_expert_ffn_route_b200 import train
 
 CSRC = M.LIB_PATH.parent.parent / "csrc"
 
@@ -135,3 +136,29 @@ def test_train_step_without_a_whole_forward_has_no_backward(no_device_switch):
                      token_mask=_FakeCuda(torch.ones(T, dtype=torch.bool)))
     with pytest.raises(RuntimeError, match="forward"):
         step.backward(_FakeCuda(torch.zeros(T, 256)))
+
+
+def test_train_step_lies_on_its_layers_device(monkeypatch):
+    """A layer on "cuda" (no index) lies where its arena does, whichever device
+    is current when the step is made: every buffer goes there, and sizes, which
+    follow the device, are asked for there."""
+    inside = []
+
+    @contextlib.contextmanager
+    def device(d):
+        inside.append(torch.device(d))
+        yield
+        inside.pop()
+    monkeypatch.setattr(torch.cuda, "device", device)
+    asked = []
+    for mod, name in [(train, n) for n in train.SIGNATURES if n.endswith("_ws_size")] + [
+            (M, n) for n in ("moe_route_ws_size", "moe_permute_ws_size", "moe_expert_ffn_ws_size")]:
+        def ask(*a, real=getattr(mod, name), name=name):
+            asked.append(name)
+            assert inside == [torch.device("meta")], name
+            return real(*a)
+        monkeypatch.setattr(mod, name, ask)
+    step = M.TrainStep(_StandIn("cuda"), T, M.MOE_BF16, balance_coef=0.5)
+    assert len(set(asked)) == 6 and not inside
+    found = [v for o in (step, step.bufs) for v in vars(o).values() if isinstance(v, torch.Tensor)]
+    assert len(found) > 20 and all(v.device.type == "meta" for v in found)
