@@ -101,6 +101,12 @@ int moe_route_backward(const float *logits, const int32_t *topk_ids, const float
  *           forward pass.  Every expert of the step has to be in `active`: a
  *           row whose expert is not, or has no blob, adds nothing to dx and
  *           gets d_topk_w 0 (a NULL blob also sets MOE_DEVERR_NULL_BLOB).
+ *           So does a row whose expert's entry is wrong (MOE_DEVERR_BAD_EXPERT,
+ *           _BAD_ROW, _MISALIGNED).  Where the lists name more rows than T k by
+ *           so much that GEMM mode cannot hold them, MOE_DEVERR_BAD_ROW is set
+ *           and no row is computed, the shared expert's neither: dx and
+ *           d_topk_w are zero.  After MOE_DEVERR_TIMEOUT the call's outputs are
+ *           not to be used.
  *  x        device [T,H]: MOE_F32 | MOE_BF16 (x_scales NULL), or MOE_Q8, the
  *           codes and x_scales of moe_act_pack8.
  *  dy       device [T,H], MOE_F32 | MOE_BF16.

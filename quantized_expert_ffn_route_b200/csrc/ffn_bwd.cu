@@ -42,7 +42,7 @@ struct GemvBwdWs {
     float *guq;     // [T*k + T, 3I]: g, u, q
     float *dwp;     // [T*k]: <q, h>
     float *dxp;     // [T*k + T, H]
-    uint8_t *ok;    // [T*k]: the row's expert was computed
+    uint8_t *ok;    // [T*k + T]: the row was computed
 };
 
 __host__ __device__ inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_first(FfnBackward a, GemvBwd
     const int chunks = a.shared ? (a.T + kNT - 1) / kNT : 0;
     const int n_items = n_act + chunks, strips = a.I / S::COLS, row_blocks = a.I / 16;
     pdl_next();
-    for (long r = static_cast<long>(blockIdx.x) * kBwThreads + threadIdx.x; r < static_cast<long>(a.T) * a.k;
+    for (long r = static_cast<long>(blockIdx.x) * kBwThreads + threadIdx.x; r < static_cast<long>(a.T) * (a.k + 1);
          r += static_cast<long>(gridDim.x) * kBwThreads)
         ws.ok[r] = 0;                              // pass 2 marks the rows it computes
     const long n_q = static_cast<long>(n_items) * strips, n_all = n_q + static_cast<long>(n_items) * row_blocks;
@@ -329,6 +329,8 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_second(FfnBackward a, GemvBw
                         ws.dwp[out0 + r0 + t] = sum;
                         ws.ok[out0 + r0 + t] = 1;
                     }
+                } else if (st == 0 && threadIdx.x == 0) {
+                    ws.ok[out0 + r0 + t] = 1;
                 }
             }
             __syncthreads();
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_second(FfnBackward a, GemvBw
 }
 
 // dx[t] = sum_j w[t,j] dxp[row(t,j)] + dxp[shared row t], in slot order, and
-// d_topk_w[t,j] = the sum of its row's shares; with `scale`, times the token's
+// d_topk_w[t,j] = the sum of its row's shares, over the rows that were computed; with `scale`, times the token's
 // sx sd and sx sx sd.  One block per token.
 __global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, const float *__restrict__ dxp,
                                                            const float *__restrict__ dwp, int shares,
@@ -349,6 +351,8 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, const 
     const size_t t = blockIdx.x;
     pdl_wait();
     const float2 sc = scale ? scale[t] : make_float2(1.f, 1.f);
+    const size_t own = static_cast<size_t>(a.T) * a.k + t;     // the shared expert's row
+    const bool shared = a.shared && ok[own];
     __shared__ int row_s[32];
     __shared__ float w_s[32];
     const int j = threadIdx.x;
@@ -387,8 +391,8 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, const 
                 acc.w = fmaf(w, v[u].w, acc.w);
             }
         }
-        if (a.shared) {
-            const float4 v = load4(dxp + (static_cast<size_t>(a.T) * a.k + t) * a.H + 4 * h4);
+        if (shared) {
+            const float4 v = load4(dxp + own * a.H + 4 * h4);
             acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         }
         acc.x = acc.x * sc.x * sc.y, acc.y = acc.y * sc.x * sc.y;
@@ -419,7 +423,7 @@ static size_t carve(int T, int k, int H, int I, uint8_t *base, GemvBwdWs *out) {
     w.guq = reinterpret_cast<float *>(take(all * 3 * I * 4));
     w.dwp = reinterpret_cast<float *>(take(rows * 4));
     w.dxp = reinterpret_cast<float *>(take(all * H * 4));
-    w.ok = take(rows);
+    w.ok = take(all);
     if (out) *out = w;
     return at;
 }

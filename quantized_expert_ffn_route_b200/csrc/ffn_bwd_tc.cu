@@ -86,7 +86,7 @@ struct TcArgs {
     const __half *x16, *dy16;     // [T, H], scaled
     float *dwp;                   // [T*k, I/32]
     float *dxp;                   // [T*k + T, H]
-    uint8_t *ok;                  // [T*k]
+    uint8_t *ok;                  // [T*k + T]
     const CUtensorMap *maps;      // [groups, 3]: Wg, Wu, Wd as bytes
     const TokTile *tiles;         // this phase's token tiles
     const int *n_tiles;
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
                     if (r < te.n) {
                         const int t = te.row0 >= 0 ? guard_index(a.perm_src[te.row0 + te.n0 + r], a.T, nullptr, 0) : te.n0 + r;
                         sx = p.scale[t].x;
-                        if (te.row0 >= 0 && m0 == 0 && ew == 0) p.ok[row0 + r] = 1;
+                        if (m0 == 0 && ew == 0) p.ok[row0 + r] = 1;
                     }
                     sx_s[r] = sx;
                 }
@@ -819,6 +819,7 @@ __global__ void __launch_bounds__(kPrepThreads, V <= 2 ? 7 : 1) k_bwd_prepare(Ff
     const size_t t = blockIdx.x - 1;
     const int h4n = a.H / 4;
     if (tid < a.k) p.ok[t * a.k + tid] = 0;
+    if (tid == 0) p.ok[static_cast<size_t>(a.T) * a.k + t] = 0;
     float4 v[2][V];                                           // x and dy, both rows' loads in flight
     uint32_t top[2] = {0, 0};
 #pragma unroll
@@ -919,7 +920,7 @@ size_t carve(int T, int k, int H, int I, int E, uint8_t *base, TcWs *out) {
     w.scale = reinterpret_cast<float2 *>(take(static_cast<size_t>(T) * sizeof(float2)));
     w.dwp = reinterpret_cast<float *>(take(rows * (I / 32) * 4));
     w.dxp = reinterpret_cast<float *>(take(all * H * 4));
-    w.ok = take(rows);
+    w.ok = take(all);
     w.tiles1 = reinterpret_cast<TokTile *>(take(p.tiles1 * sizeof(TokTile)));
     w.tiles2 = reinterpret_cast<TokTile *>(take(p.tiles2 * sizeof(TokTile)));
     w.counts = reinterpret_cast<int *>(take(2 * sizeof(int)));

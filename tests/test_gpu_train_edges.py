@@ -70,3 +70,93 @@ def test_balance_and_router_workspace_at_any_16_bytes(E):
     assert M.moe_device_error() == 0
     for o in outs[1:]:
         assert all(torch.equal(p, q) for p, q in zip(outs[0], o))
+
+
+# ------------------------------------------------- rows that nobody computes
+def _with_guards(c, mode, xkind=F32):
+    """c.run with guard bytes around its workspace, which starts 16 bytes into a buffer."""
+    s = _Scratch(M.moe_expert_ffn_backward_ws_size(c.bits, c.T, c.k, c.H, c.I, c.E, mode), 16)
+    out = c.run(xkind, F32, F32, mode, ws=s.ws)
+    s.check()
+    return out
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("T", [1, 2, 3, 33])
+def test_expert_backward_one_expert_listed_for_all(T, mode):
+    """`active` names one expert over and over, and it has all the rows: while
+    the lists hold them, every row is that expert's; where they do not, nothing
+    is computed and nothing is added, whatever the workspace held."""
+    c = _Case(4, T, 2, 128, 128, 64, True, 43)
+    off, act, src, dst = c.perm
+    n, e = int(act[0]), int(act[1])
+    act = act.clone()
+    act[1:1 + n] = e
+    off = torch.zeros_like(off)
+    off[e + 1:] = 2 * T
+    c.perm = (off, act, src, dst)
+    dx, dw = _with_guards(c, mode)
+    if mode == M.MOE_MODE_GEMM and T == 33:                # 64 times 66 rows
+        assert M.moe_device_error() == M.DEVERR_BAD_ROW
+        assert (dx == 0).all() and (dw == 0).all()
+    else:
+        assert M.moe_device_error() == 0
+        c.ids[:] = e
+        c.check(dx, dw, F32, mode)
+
+
+BAD_LISTS = ["offsets beyond the rows", "offsets that fall", "expert number too large", "expert number negative",
+             "blob off by 8 bytes"]
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("T", [1, 3, 33])
+@pytest.mark.parametrize("bad", BAD_LISTS)
+def test_expert_backward_reports_bad_lists(bad, T, mode):
+    """One expert's entry is wrong: it is reported in both forms, its rows add
+    nothing and the others are exact."""
+    c = _Case(4, T, 2, 128, 128, 6, True, 44)
+    off, act, src, dst = (t.clone() for t in c.perm)
+    last = int(act[0])
+    e = int(act[last])                                     # the last active expert: its end is nobody's start
+    table = c.layer.table.clone()
+    want = M.DEVERR_BAD_ROW
+    if bad == "offsets beyond the rows":
+        off[e + 1] = 2 * T + 1
+    elif bad == "offsets that fall":
+        off[e + 1] = 0
+    elif bad == "blob off by 8 bytes":
+        table[e] += 8
+        want = M.DEVERR_MISALIGNED
+    else:
+        act[last] = 6 if bad == "expert number too large" else -1
+        want = M.DEVERR_BAD_EXPERT
+    c.perm = (off, act, src, dst)
+    s = _Scratch(M.moe_expert_ffn_backward_ws_size(4, T, 2, 128, 128, 6, mode), 16)
+    dx, dw = c.run(F32, F32, F32, mode, table=table, ws=s.ws)
+    s.check()
+    assert M.moe_device_error() == want
+    _, gw = c.check(dx, dw, F32, mode, skip=(e,))
+    assert (gw[c.ids == e] == 0).all()
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_expert_backward_reports_rows_outside_the_permutation(mode):
+    T, k = 9, 2
+    c = _Case(4, T, k, 128, 128, 6, True, 45)
+    off, act, src, dst = (t.clone() for t in c.perm)
+    dst[3], dst[10] = T * k, -1
+    c.perm = (off, act, src, dst)
+    dx, dw = _with_guards(c, mode)
+    assert M.moe_device_error() == M.DEVERR_BAD_ROW
+    at = [divmod(3, k), divmod(10, k)]
+    assert all(float(dw[t, j]) == 0 for t, j in at)
+    for t, j in at:
+        c.w[t, j] = 0                                      # no share of dx
+    rx, rw, ex, ew = R.experts_backward(4, 128, 128, c.blobs, c.shared, c.ids, c.w, c.xv, c.dyv,
+                                        0.0 if mode == M.MOE_MODE_GEMV else R.U16)
+    assert (np.abs(dx.double().cpu().numpy() - rx) <= ex + R.U32 * np.abs(rx) + 1e-37).all()
+    keep = np.ones((T, k), bool)
+    for t, j in at:
+        keep[t, j] = False
+    assert (np.abs(dw.double().cpu().numpy() - rw) <= ew + 1e-37)[keep].all()
