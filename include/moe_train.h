@@ -113,12 +113,18 @@ int moe_route_backward(const float *logits, const int32_t *topk_ids, const float
  *  dx       device [T,H] out, MOE_F32 | MOE_BF16 (rounded once).
  *  d_topk_w device [T,k] fp32 out.
  *  mode     MOE_MODE_GEMV: CUDA cores, fp32 throughout, any T.
- *           MOE_MODE_GEMM: tcgen05 tensor cores.  Operands are fp16: the
- *           weights, and each token's x and dy divided by a power of two of its
- *           own (undone in fp32 at the end), so that neither's scale matters;
- *           the gradients of g and u are rounded to fp16 between the two
- *           products.  fp32 accumulation.  Blobs in device memory.
- *           MOE_MODE_AUTO: GEMV up to 4 tokens, else GEMM.
+ *           MOE_MODE_GEMM: tcgen05 tensor cores.  Operands are rounded to
+ *           fp16 (half a step: 2^-11 of the value): the weights, each token's x
+ *           and dy, and, between the two products, the gradients of g and u.
+ *           x and dy are divided by a power of two of the token's own, the
+ *           gradients of g and u by one of the token's and one of the expert's
+ *           (all undone in fp32), so that neither x's, dy's nor the weights'
+ *           scale matters and nothing leaves fp16's range, but for a weight
+ *           that is itself outside: a step above 65504 / 2^(bits-1), infinite
+ *           or NaN sets MOE_DEVERR_NONFINITE, and the rows of its expert may
+ *           not be finite.  fp32 accumulation.  Blobs in device memory.
+ *           MOE_MODE_AUTO: GEMV up to 4 tokens, else GEMM, with its fp16
+ *           operands; a caller that wants fp32 throughout asks for GEMV.
  *  Shapes as for moe_expert_ffn_*: H a multiple of 128 up to 8192, I up to 4096.
  *  ws: at least moe_expert_ffn_backward_ws_size(...) bytes. */
 size_t moe_expert_ffn_backward_ws_size(int bits, int T, int k, int H, int I, int E, int mode);

@@ -343,18 +343,26 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_second(FfnBackward a, GemvBw
 
 // dx[t] = sum_j w[t,j] dxp[row(t,j)] + dxp[shared row t], in slot order, and
 // d_topk_w[t,j] = the sum of its row's shares, over the rows that were computed; with `scale`, times the token's
-// sx sd and sx sx sd.  One block per token.
+// sx sd / r and sx sx sd.  One block per token.
 __global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, const float *__restrict__ dxp,
                                                            const float *__restrict__ dwp, int shares,
                                                            const uint8_t *__restrict__ ok,
-                                                           const float2 *__restrict__ scale) {
+                                                           const float4 *__restrict__ scale) {
     const size_t t = blockIdx.x;
     pdl_wait();
-    const float2 sc = scale ? scale[t] : make_float2(1.f, 1.f);
+    const float4 sc = scale ? scale[t] : make_float4(1.f, 1.f, 1.f, 1.f);
     const size_t own = static_cast<size_t>(a.T) * a.k + t;     // the shared expert's row
-    const bool shared = a.shared && ok[own];
     __shared__ int row_s[32];
     __shared__ float w_s[32];
+    // what a column needs once, at its end, is read from shared memory there: in
+    // registers it leaves room for four blocks an SM instead of five (156 us for
+    // 144 at 8192 x 2048, top-10)
+    __shared__ float end_s[4];                     // 1 where the shared row was computed; 1/r, sx, sd
+    const volatile float *end = end_s;
+    if (threadIdx.x == 32) {
+        end_s[0] = a.shared && ok[own] ? 1.f : 0.f;
+        end_s[1] = sc.w, end_s[2] = sc.x, end_s[3] = sc.y;
+    }
     const int j = threadIdx.x;
     if (j < a.k) {
         int row = a.perm_dst[t * a.k + j];
@@ -391,12 +399,15 @@ __global__ void __launch_bounds__(kBwThreads) k_bwd_gather(FfnBackward a, const 
                 acc.w = fmaf(w, v[u].w, acc.w);
             }
         }
-        if (shared) {
+        if (end[0] != 0.f) {
             const float4 v = load4(dxp + own * a.H + 4 * h4);
             acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         }
-        acc.x = acc.x * sc.x * sc.y, acc.y = acc.y * sc.x * sc.y;
-        acc.z = acc.z * sc.x * sc.y, acc.w = acc.w * sc.x * sc.y;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            const float f = end[i];
+            acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+        }
         const size_t at = t * (a.H / 4) + h4;
         if (a.dx_dtype == MOE_BF16) {
             __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
@@ -458,7 +469,7 @@ static int launch_gemv_bwd(const FfnBackward &a, const GemvBwdWs &w, cudaStream_
 }
 
 int launch_ffn_backward_gather(const FfnBackward &a, const float *dxp, const float *dwp, int shares,
-                               const uint8_t *ok, const float2 *scale, cudaStream_t s) {
+                               const uint8_t *ok, const float4 *scale, cudaStream_t s) {
     const int rc = cuda_status(launch_after(k_bwd_gather, dim3(a.T), kBwThreads, 0, s, a, dxp, dwp, shares, ok, scale),
                                "expert backward gather launch");
     if (!rc) count_launches(1);

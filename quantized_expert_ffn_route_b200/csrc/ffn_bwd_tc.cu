@@ -15,7 +15,16 @@
 // range independent of either's scale; g is scaled back in fp32 before the
 // activation, and dg, du are kept in the scaled form,
 //   dg / (sx sd) = q' u' (s + a (1 - s)),   du / (sx sd) = q' a',
-// until the gather multiplies by w sx sd in fp32.
+// times c r, until the gather multiplies by w sx sd / r in fp32.  c (a power of
+// two of the expert, undone as phase 2 writes its fp32 rows) and r (one of the
+// token) hold them in fp16's range whatever the weights are: with D the largest
+// magnitude of a code,
+//   |u'|, |a'| <= D max|step of Wg, Wu| |x'|_1,   |q'| <= D max|step of Wd| |dy'|_1,
+// each factor is taken up to a power of two, c r times their product is 2^15,
+// and |s + a (1 - s)| < 1.1.  So none is infinite, and one that is 2^-29 of the
+// bound still has all its bits: for random weights of one size values lie
+// about 2^13 to 2^15 below it.  The steps' largest are read ahead, with the
+// rows: a sixteenth of a weight a byte (4 bits: 1/9 of the weights' bytes).
 // They lie transposed between the phases, [2I] x rows, a group's rows padded
 // to 16: a thread of phase 1 holds one i and 16 rows, 32 bytes to store, and
 // phase 2 takes its N side MN-major as it takes the weights.
@@ -40,8 +49,8 @@
 // and TMEM is freed).
 //
 // Measured (512 experts of 2048 x 512 and a shared one, top-10, 4 bits, 8192
-// tokens): preparation 33 us, phase 1 775, phase 2 525, gather 141; 945 GFLOP at
-// 640 TFLOP/s.  No role alone bounds the two phases: of phase 1's, copying no rows
+// tokens): preparation 56 us (33 of it the rows, the rest 100 MB of steps), phase
+// 1 790, phase 2 527, gather 144; 945 GFLOP at 623 TFLOP/s.  No role alone bounds the two phases: of phase 1's, copying no rows
 // saves 27, writing no transposed tiles 37, the epilogue's work 120, the MMAs 34;
 // of phase 2's, its stores 78, its codes 55, its B copies 55, its MMAs 65.  A tile
 // of 128 rows (phase 1) leaves room for three B stages and fills TMEM with its
@@ -80,7 +89,9 @@ struct __align__(16) TokTile {
 
 struct TcArgs {
     FfnBackward a;
-    const float2 *scale;          // [T]: sx, sd
+    const float4 *scale;          // [T]: sx, sd, r, 1/r
+    const uint32_t *steps;        // [groups, 32]: largest steps of Wg and Wu (16), of Wd (16), by parts
+    int gu_parts, d_parts;
     __half *gu16;                 // [2I, cols]: dg, du, scaled, a column per row of a group
     int cols;
     const __half *x16, *dy16;     // [T, H], scaled
@@ -128,7 +139,7 @@ struct Cfg {
     static constexpr uint32_t OFF_B = SA * A_STAGE;
     static constexpr uint32_t OFF_RAW = OFF_B + SB * B_STAGE;
     static constexpr uint32_t OFF_SX = OFF_RAW + (PHASE == 1 ? SR * RAW_SLOT : 0);
-    static constexpr uint32_t OFF_BAR = OFF_SX + (PHASE == 1 ? EPI * MAXN * 4 : 0);   // a copy per epilogue warp
+    static constexpr uint32_t OFF_BAR = OFF_SX + (PHASE == 1 ? EPI * MAXN * 8 : 0);   // a copy per epilogue warp
     static constexpr uint32_t SMEM = OFF_BAR + kBars * 8 + 16 + 1024;
     static_assert(SMEM <= kSmemMax, "shared memory per block");
     static_assert(2 * SA + 2 * SB + 2 * SR + 5 <= kBars, "barrier slots");
@@ -244,6 +255,23 @@ __device__ __forceinline__ void block_words(const Codes<BITS> &c, __half d, uint
         }
     }
 }
+
+// e with c = 2^e of a group's inner gradients (a warp's call): 15 less the
+// exponents of the bound's two factors.  0 where no bound is to be had (a step
+// that is infinite or NaN) or none is needed (all steps of a side are 0).
+template <int BITS>
+__device__ __forceinline__ int group_exponent(const TcArgs &p, int g) {
+    const int lane = threadIdx.x & 31, part = lane & 15;
+    const uint32_t v = part < (lane < 16 ? p.gu_parts : p.d_parts) ? p.steps[32 * static_cast<size_t>(g) + lane] : 0u;
+    const uint32_t gu = __reduce_max_sync(0xffffffffu, lane < 16 ? v : 0u);
+    const uint32_t d = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : v);
+    if (gu == 0u || d == 0u || gu >= 0x7C00u || d >= 0x7C00u) return 0;
+    auto up = [](uint32_t h) {                    // the smallest e with the step below 2^e
+        return static_cast<int>(__float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h)))) >> 23) - 126;
+    };
+    return 15 - 2 * (BITS - 1) - up(gu) - up(d);
+}
+__device__ __forceinline__ float exp2_of(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // What a dequantising thread reads for one stage: four blocks and their steps.
 template <int BITS> struct Step {
@@ -566,20 +594,22 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
         static_assert(kEpi0 % 4 == 0, "TMEM lanes follow the warp's rank");
         const int ew = warp - kEpi0, q = ew & 3;              // TMEM lanes 32q .. 32q + 31
         const int m = 32 * q + block_order<BITS>(lane);       // the weight row (column) of this lane
-        // each warp has its own table of the tile's scales: no barrier among
-        // them, of which one may leave early
-        float *sx_s = reinterpret_cast<float *>(smem + C::OFF_SX) + ew * MAXN;
+        // each warp has its own table of the tile's scales (sx, c r): no barrier
+        // among them, of which one may leave early
+        float2 *sx_s = reinterpret_cast<float2 *>(smem + C::OFF_SX) + ew * MAXN;
         for (int i = 0; i < n_my; ++i) {
             int m0;
             const TokTile te = tile_of(i, m0);
             const size_t row0 = static_cast<size_t>(te.row0 >= 0 ? te.row0 : a.T * a.k) + te.n0;
+            const int ce = group_exponent<BITS>(p, te.g);
             if constexpr (PHASE == 1) {
                 __syncwarp();                                 // the last tile's scales are read
                 for (int r = lane; r < ((te.n + 15) & ~15); r += 32) {
-                    float sx = 0.f;
+                    float2 sx = make_float2(0.f, 0.f);
                     if (r < te.n) {
                         const int t = te.row0 >= 0 ? guard_index(a.perm_src[te.row0 + te.n0 + r], a.T, nullptr, 0) : te.n0 + r;
-                        sx = p.scale[t].x;
+                        const float4 sc = p.scale[t];
+                        sx = make_float2(sc.x, exp2_of(ce) * sc.z);
                         if (m0 == 0 && ew == 0) p.ok[row0 + r] = 1;
                     }
                     sx_s[r] = sx;
@@ -601,15 +631,16 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
                     uint32_t dg[4], du[4];
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
-                        const float2 sx = *reinterpret_cast<const float2 *>(sx_s + c0 + e);
+                        const float4 sx = *reinterpret_cast<const float4 *>(sx_s + c0 + e);
                         float vg[2], vu[2];
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const float g = gv[e + x] * (x ? sx.y : sx.x);
+                            const float g = gv[e + x] * (x ? sx.z : sx.x);
                             const float s = __fdividef(1.f, 1.f + __expf(-g));
-                            const float qu = qv[e + x] * uv[e + x], act = gv[e + x] * s;        // a / sx
+                            const float q2 = qv[e + x] * (x ? sx.w : sx.y);
+                            const float qu = q2 * uv[e + x], act = gv[e + x] * s;               // a / sx
                             vg[x] = qu * fmaf(g * s, 1.f - s, s);
-                            vu[x] = qv[e + x] * act;
+                            vu[x] = q2 * act;
                             qv[e + x] = qu * act;
                         }
                         const __half2 hg = __floats2half2_rn(vg[0], vg[1]), hu = __floats2half2_rn(vu[0], vu[1]);
@@ -634,14 +665,20 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
                         float sum = qv[0] + __shfl_xor_sync(0xffffffffu, qv[0], 2);
                         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                         const int r = c0 + (lane >> 2);
-                        if (!(lane & 3) && r < te.n) p.dwp[(row0 + r) * (I / 32) + m0 / 32 + q] = sum;
+                        if (!(lane & 3) && r < te.n) {
+                            const float inv = __uint_as_float(0x7F000000u - __float_as_uint(sx_s[r].y));   // 1 / (c r)
+                            p.dwp[(row0 + r) * (I / 32) + m0 / 32 + q] = sum * inv;
+                        }
                     }
                 }
             } else {
+                const float inv = exp2_of(-ce);
                 for (int c0 = 0; c0 < te.n; c0 += 16) {
                     float v[16];
                     tmem_ld16(base + c0, v);
                     tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] *= inv;
                     float *out = p.dxp + (row0 + c0) * H + m0 + m;
                     if (c0 + 16 <= te.n) {
 #pragma unroll
@@ -715,11 +752,14 @@ __global__ void __launch_bounds__(Cfg<BITS, PHASE, MAXN>::THREADS, 1) k_bwd_tc(
 // ------------------------------------------------------------------ prepare
 namespace {
 constexpr int kPrepThreads = 256;
+constexpr int kStepLoads = 8;     // 16-byte loads of steps a thread has in flight
 
 struct Prep {
     __half *x16, *dy16;
-    float2 *scale;
+    float4 *scale;
     uint8_t *ok;
+    uint32_t *steps;              // [groups, 32]
+    int gu_parts, d_parts;        // parts of a group's steps, a block each
     TokTile *tiles1, *tiles2;
     int *counts;                  // token tiles of phase 1 and 2
     int max1, max2;               // tokens per tile
@@ -737,6 +777,14 @@ __device__ __forceinline__ float2 row_scale(uint32_t top) {
     return make_float2(__uint_as_float((254u - e) << 23), __uint_as_float(e << 23));
 }
 
+// e with the sum of the scaled row's |values| below 2^e (its largest is in
+// [1, 2), but for the ends of the range), from the plain row's sum and scale:
+// 15 covers H = 8192 where the plain sum is beyond fp32.  0 for a row of zeros.
+__device__ __forceinline__ int sum_exponent(float sum, float scale) {
+    const int s = static_cast<int>(__float_as_uint(sum) >> 23), e = static_cast<int>(__float_as_uint(scale) >> 23);
+    return s >= 255 ? 15 : min(max(s + 1 - e, 0), 15);
+}
+
 // Tiles of a group of n rows: as few as hold it, of equal size (a multiple of
 // 16), so that no tile is left with a few rows.
 __device__ __forceinline__ int tile_rows(int n, int most) {
@@ -746,15 +794,18 @@ __device__ __forceinline__ int tile_rows(int n, int most) {
 }  // namespace
 
 // Block 0 lists both phases' token tiles, the next T blocks scale and round one
-// token's x and dy each, and the rest make the maps of the experts' codes.
+// token's x and dy each, and the rest find the experts' largest steps, a part of
+// a group's each, and make the maps of their codes.
 // V: float4 a thread holds of a row.
-// V = 2 is held to seven blocks an SM, a few registers spilled: 33 us at
-// 8192 x 2048, for 48 with five blocks and none spilled.
+// V = 2 is held to seven blocks an SM, a few registers spilled: the rows take
+// 33 us at 8192 x 2048, for 48 with five blocks and none spilled.  Eight loads of
+// steps in flight: 56 us with 512 experts' steps, 59 with four, 71 with two.
 template <int V>
 __global__ void __launch_bounds__(kPrepThreads, V <= 2 ? 7 : 1) k_bwd_prepare(FfnBackward a, Prep p,
                                                               const __grid_constant__ CUtensorMap rows_map,
                                                               const __grid_constant__ CUtensorMap down_map) {
     __shared__ uint32_t part[2][kPrepThreads / 32];
+    __shared__ float part_sum[2][kPrepThreads / 32];
     __shared__ int3 sums[kPrepThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (blockIdx.x == 0) {
@@ -803,17 +854,46 @@ __global__ void __launch_bounds__(kPrepThreads, V <= 2 ? 7 : 1) k_bwd_prepare(Ff
     }
     pdl_next();
     if (static_cast<int>(blockIdx.x) > a.T) {
-        // a warp per group: the maps of its three matrices' codes
-        const int g = (static_cast<int>(blockIdx.x) - a.T - 1) * (kPrepThreads / 32) + warp;
+        const int parts = p.gu_parts + p.d_parts, v = static_cast<int>(blockIdx.x) - a.T - 1;
+        const int g = v / parts, at = v - g * parts;
         const int n_act = guard_count(a.active[0], min(a.E, a.T * a.k), nullptr);
         if (g >= n_act + (a.shared ? 1 : 0)) return;
         const BwdGroup G = bwd_group(a, g, n_act, false);
         if (G.n <= 0) return;
         const BlobView bv = blob_view(G.blob, a.bits, a.H, a.I);
-        CUtensorMap *to = p.maps + 3 * static_cast<size_t>(g);
-        map_for(to, rows_map, bv.cg);
-        map_for(to + 1, rows_map, bv.cu);
-        map_for(to + 2, down_map, bv.cd);
+        if (at == 0 && warp == 0) {                           // the maps of the three matrices' codes
+            CUtensorMap *to = p.maps + 3 * static_cast<size_t>(g);
+            map_for(to, rows_map, bv.cg);
+            map_for(to + 1, rows_map, bv.cu);
+            map_for(to + 2, down_map, bv.cd);
+        }
+        const bool down = at >= p.gu_parts;
+        const int i = down ? at - p.gu_parts : at, most = down ? p.d_parts : p.gu_parts;
+        const long n8 = static_cast<long>(down ? 1 : 2) * a.H * a.I / 32 / 8;               // eight steps a load
+        const uint4 *steps = reinterpret_cast<const uint4 *>(down ? bv.sd : bv.sg);         // Wu's lie behind Wg's
+        const long end = n8 * (i + 1) / most;
+        uint32_t top2 = 0;
+        for (long j = n8 * i / most + tid; j < end; j += kStepLoads * kPrepThreads) {
+            uint4 u[kStepLoads];
+#pragma unroll
+            for (int x = 0; x < kStepLoads; ++x)
+                u[x] = j + x * kPrepThreads < end ? __ldg(steps + j + x * kPrepThreads) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < kStepLoads; ++x) {
+                top2 = __vmaxu2(__vmaxu2(top2, u[x].x & 0x7FFF7FFFu), u[x].y & 0x7FFF7FFFu);
+                top2 = __vmaxu2(__vmaxu2(top2, u[x].z & 0x7FFF7FFFu), u[x].w & 0x7FFF7FFFu);
+            }
+        }
+        const uint32_t most1 = __reduce_max_sync(0xffffffffu, max(top2 & 0xFFFFu, top2 >> 16));
+        if (lane == 0) part[0][warp] = most1;
+        __syncthreads();
+        if (tid == 0) {
+            uint32_t m = 0;
+            for (int w = 0; w < kPrepThreads / 32; ++w) m = max(m, part[0][w]);
+            p.steps[32 * static_cast<size_t>(g) + (down ? 16 : 0) + i] = m;
+            // a step whose lowest code's weight is beyond fp16: 65504 / 2^(bits - 1) and up
+            if (m > 0x7BFFu - (static_cast<uint32_t>(a.bits - 1) << 10)) report(a.err, MOE_DEVERR_NONFINITE);
+        }
         return;
     }
     const size_t t = blockIdx.x - 1;
@@ -822,6 +902,7 @@ __global__ void __launch_bounds__(kPrepThreads, V <= 2 ? 7 : 1) k_bwd_prepare(Ff
     if (tid == 0) p.ok[static_cast<size_t>(a.T) * a.k + t] = 0;
     float4 v[2][V];                                           // x and dy, both rows' loads in flight
     uint32_t top[2] = {0, 0};
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int h4 = tid + i * kPrepThreads;
@@ -837,9 +918,11 @@ __global__ void __launch_bounds__(kPrepThreads, V <= 2 ? 7 : 1) k_bwd_prepare(Ff
             const float4 &u = v[which][i];
             top[which] = max(max(top[which], __float_as_uint(fabsf(u.x))), __float_as_uint(fabsf(u.y)));
             top[which] = max(max(top[which], __float_as_uint(fabsf(u.z))), __float_as_uint(fabsf(u.w)));
+            sum[which] += (fabsf(u.x) + fabsf(u.y)) + (fabsf(u.z) + fabsf(u.w));
         }
         top[which] = __reduce_max_sync(0xffffffffu, top[which]);
-        if (lane == 0) part[which][warp] = top[which];
+        sum[which] = warp_sum(sum[which]);
+        if (lane == 0) part[which][warp] = top[which], part_sum[which][warp] = sum[which];
     }
     __syncthreads();
     float2 scale[2];
@@ -863,7 +946,17 @@ __global__ void __launch_bounds__(kPrepThreads, V <= 2 ? 7 : 1) k_bwd_prepare(Ff
             out[which ? h4 : (h4 & ~7) + block_place(a.bits, h4 & 7) / 4] = o;
         }
     }
-    if (tid == 0) p.scale[t] = make_float2(scale[0].y, scale[1].y);
+    if (tid == 0) {
+        int e = 0;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kPrepThreads / 32; ++w) s += part_sum[which][w];
+            if (top[which] < 0x7F800000u) e += sum_exponent(s, scale[which].y);
+        }
+        p.scale[t] = make_float4(scale[0].y, scale[1].y, exp2_of(-e), exp2_of(e));
+    }
 }
 
 // ------------------------------------------------------------------ launch
@@ -874,10 +967,11 @@ struct TcPlan {
     size_t tiles1, tiles2;        // bounds on the token tiles
     size_t cols;                  // and on the rows, each group's padded to 16
     size_t groups;
+    int gu_parts, d_parts;        // blocks that look through a group's steps
 };
 constexpr int kSmallN = 64, kLargeN1 = 128, kLargeN2 = 256;
 
-TcPlan plan_of(int T, int k, int E) {
+TcPlan plan_of(int T, int k, int H, int I, int E) {
     const long rows = static_cast<long>(T) * k, groups = rows < E ? rows : E;
     TcPlan p;
     p.large = rows > 32L * groups;
@@ -889,12 +983,20 @@ TcPlan plan_of(int T, int k, int E) {
     p.tiles2 = bound(p.max2);
     p.groups = static_cast<size_t>(groups + 1);
     p.cols = static_cast<size_t>((rows + T + 15 * (groups + 1) + 63) / 64 * 64);
+    // a part is one round of a block's loads (32 KB), or a sixteenth
+    auto parts = [&](long steps) {
+        const long n = (steps / 8 + kStepLoads * kPrepThreads - 1) / (kStepLoads * kPrepThreads);
+        return static_cast<int>(n < 16 ? n : 16);
+    };
+    p.gu_parts = parts(2L * H * I / 32);
+    p.d_parts = parts(1L * H * I / 32);
     return p;
 }
 
 struct TcWs {
     __half *x16, *dy16, *gu16;
-    float2 *scale;
+    float4 *scale;
+    uint32_t *steps;
     float *dwp, *dxp;
     uint8_t *ok;
     TokTile *tiles1, *tiles2;
@@ -906,7 +1008,7 @@ struct TcWs {
 // need 128), each at a multiple of kWsAlign; returns their bytes.
 size_t carve(int T, int k, int H, int I, int E, uint8_t *base, TcWs *out) {
     const size_t rows = static_cast<size_t>(T) * k, all = rows + T;
-    const TcPlan p = plan_of(T, k, E);
+    const TcPlan p = plan_of(T, k, H, I, E);
     size_t at = 0;
     auto take = [&](size_t n) {
         uint8_t *q = base ? base + at : nullptr;
@@ -917,7 +1019,8 @@ size_t carve(int T, int k, int H, int I, int E, uint8_t *base, TcWs *out) {
     w.x16 = reinterpret_cast<__half *>(take(static_cast<size_t>(T) * H * 2));
     w.dy16 = reinterpret_cast<__half *>(take(static_cast<size_t>(T) * H * 2));
     w.gu16 = reinterpret_cast<__half *>(take(p.cols * 2 * I * 2));
-    w.scale = reinterpret_cast<float2 *>(take(static_cast<size_t>(T) * sizeof(float2)));
+    w.scale = reinterpret_cast<float4 *>(take(static_cast<size_t>(T) * sizeof(float4)));
+    w.steps = reinterpret_cast<uint32_t *>(take(p.groups * 32 * sizeof(uint32_t)));
     w.dwp = reinterpret_cast<float *>(take(rows * (I / 32) * 4));
     w.dxp = reinterpret_cast<float *>(take(all * H * 4));
     w.ok = take(all);
@@ -949,7 +1052,7 @@ size_t ffn_backward_gemm_ws_bytes(int T, int k, int H, int I, int E) {
 
 bool ffn_backward_gemm_supported(int T, int k, int H, int I, int E) {
     // tile and step numbers are ints
-    const TcPlan p = plan_of(T, k, E);
+    const TcPlan p = plan_of(T, k, H, I, E);
     const double n1 = static_cast<double>(p.tiles1) * (I / kBM), n2 = static_cast<double>(p.tiles2) * (H / kBM);
     if (p.cols > 2000000000u) return false;
     return n1 < 2e9 && n2 < 2e9 && (n1 / num_sms() + 1) * (H / kBK) < 2e9 && (n2 / num_sms() + 1) * (I / kBK) < 2e9;
@@ -958,8 +1061,8 @@ bool ffn_backward_gemm_supported(int T, int k, int H, int I, int E) {
 int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     TcWs w;
     carve(a.T, a.k, a.H, a.I, a.E, ws_start(ws), &w);
-    const TcPlan plan = plan_of(a.T, a.k, a.E);
-    const Prep prep = {w.x16, w.dy16, w.scale, w.ok, w.tiles1, w.tiles2, w.counts, plan.max1, plan.max2,
+    const TcPlan plan = plan_of(a.T, a.k, a.H, a.I, a.E);
+    const Prep prep = {w.x16, w.dy16, w.scale, w.ok, w.steps, plan.gu_parts, plan.d_parts, w.tiles1, w.tiles2, w.counts, plan.max1, plan.max2,
                        static_cast<int>(plan.tiles1), static_cast<int>(plan.tiles2),
                        static_cast<int>(plan.cols), w.maps};
     // (the base is a stand-in: each group's maps get their own)
@@ -968,7 +1071,7 @@ int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     int rc = make_byte_map(&rows_map, w.x16, a.I, rowb, kBM, kBK * a.bits / 8);
     if (!rc) rc = make_byte_map(&down_map, w.x16, a.H, downb, kBK, kBM * a.bits / 8);
     if (rc) return rc;
-    const unsigned blocks = static_cast<unsigned>(a.T + 1 + (plan.groups + kPrepThreads / 32 - 1) / (kPrepThreads / 32));
+    const unsigned blocks = static_cast<unsigned>(a.T + 1 + plan.groups * (plan.gu_parts + plan.d_parts));
     if (a.H <= 2048) k_bwd_prepare<2><<<blocks, kPrepThreads, 0, s>>>(a, prep, rows_map, down_map);
     else k_bwd_prepare<8><<<blocks, kPrepThreads, 0, s>>>(a, prep, rows_map, down_map);
     count_launches(1);
@@ -976,7 +1079,7 @@ int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s) {
     if (rc) return rc;
     const long long hook = test_hook_value(MOE_HOOK_WAIT_LIMIT_NS);
     const unsigned long long limit = hook > 0 ? static_cast<unsigned long long>(hook) : kWaitNs;
-    const TcArgs p = {a, w.scale, w.gu16, static_cast<int>(plan.cols), w.x16, w.dy16, w.dwp, w.dxp, w.ok, w.maps,
+    const TcArgs p = {a, w.scale, w.steps, plan.gu_parts, plan.d_parts, w.gu16, static_cast<int>(plan.cols), w.x16, w.dy16, w.dwp, w.dxp, w.ok, w.maps,
                       w.tiles1, w.counts, limit};
     TcArgs p2 = p;
     p2.tiles = w.tiles2, p2.n_tiles = w.counts + 1;

@@ -40,10 +40,11 @@ size_t ffn_backward_gemm_ws_bytes(int T, int k, int H, int I, int E);
 bool ffn_backward_gemm_supported(int T, int k, int H, int I, int E);
 int launch_ffn_backward_gemm(const FfnBackward &a, void *ws, cudaStream_t s);
 // dx and d_topk_w from the rows' parts: dxp [T*k + T, H], dwp [T*k, shares], ok
-// [T*k + T] (rows that were computed: the others' parts are not read); scale [T] (sx, sd) where the parts are kept
-// divided by sx sd (dwp: by sx sx sd), or NULL.
+// [T*k + T] (rows that were computed: the others' parts are not read); scale
+// [T] (sx, sd, r, 1/r) where dxp is kept times r / (sx sd) and dwp divided by
+// sx sx sd, or NULL.
 int launch_ffn_backward_gather(const FfnBackward &a, const float *dxp, const float *dwp, int shares,
-                               const uint8_t *ok, const float2 *scale, cudaStream_t s);
+                               const uint8_t *ok, const float4 *scale, cudaStream_t s);
 
 struct RouterBackward {
     const void *dl, *x, *w;

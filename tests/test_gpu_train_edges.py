@@ -160,3 +160,111 @@ def test_expert_backward_reports_rows_outside_the_permutation(mode):
     for t, j in at:
         keep[t, j] = False
     assert (np.abs(dw.double().cpu().numpy() - rw) <= ew + 1e-37)[keep].all()
+
+
+# ------------------------------------------------------ range of the weights
+def _steps(c, blob):
+    """The blob's steps, fp16: gate's and up's, then down's."""
+    n = c.H * c.I // 32
+    s = blob[3 * c.H * c.I * c.bits // 8:].view(np.float16)
+    return s[:2 * n], s[2 * n:]
+
+
+def _rescale(c, change):
+    """Changes every blob's steps in place and lays the experts out again."""
+    for blob in list(c.blobs) + ([] if c.shared is None else [c.shared]):
+        change(*_steps(c, blob))
+    c.layer = M.MoELayer(c.bits, c.H, c.I, c.E, c.k, c.blobs, c.shared)
+
+
+def _check_weights(c, dx, dw, mode):
+    """c.check with one more term.  The gradients of g and u are stored in fp16
+    times a power of two 2^15 / B' with B' at most 16 times their bound
+    B = half^2 max|step of gate, up| max|step of down| |x|_1 |dy|_1 (four factors,
+    each taken up to a power of two).  fp16's smallest step is 2^-24: a stored
+    value is off by up to 2^-25 2^-15 16 B = 2^-36 B."""
+    gemm = mode == M.MOE_MODE_GEMM
+    rx, rw, ex, ew = R.experts_backward(c.bits, c.H, c.I, c.blobs, c.shared, c.ids, c.w, c.xv, c.dyv,
+                                        R.U16 if gemm else 0.0)
+    if gemm:
+        l1 = np.abs(c.xv).sum(1) * np.abs(c.dyv).sum(1)
+        for e in range(c.E + (c.shared is not None)):
+            blob = c.blobs[e] if e < c.E else c.shared
+            gu, d = (float(np.abs(s.astype(np.float64)).max()) for s in _steps(c, blob))
+            floor = 2.0 ** -36 * 4.0 ** (c.bits - 1) * gu * d * l1
+            Wg, Wu, _ = R.matrices(c.bits, c.H, c.I, blob)
+            col = np.abs(Wg).sum(0) + np.abs(Wu).sum(0)
+            wt = np.where(c.ids == e, c.w, 0).sum(1) if e < c.E else 1.0
+            ex = ex + 1.1 * (wt * floor)[:, None] * col
+    gx, gw = dx.double().cpu().numpy(), dw.double().cpu().numpy()
+    assert np.isfinite(gx).all() and np.isfinite(gw).all()
+    assert (np.abs(gx - rx) <= ex + 1e-37).all(), (np.abs(gx - rx) / (ex + 1e-37)).max()
+    assert (np.abs(gw - rw) <= ew + 1e-37).all(), (np.abs(gw - rw) / (ew + 1e-37)).max()
+    # as in c.check: about ten independent roundings of half a step along a value's path
+    rms = np.sqrt(10.0) * (R.U16 if gemm else 32 * R.U32)
+    assert np.linalg.norm(gx - rx) <= rms * np.linalg.norm(rx)
+    assert np.linalg.norm(gw - rw) <= rms * np.linalg.norm(rw)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("gu,down", [(-9, -9), (-9, 9), (6, 6), (12, 16), (16, -9)])
+@pytest.mark.parametrize("bits,T,E", [(4, 20, 6), (2, 20, 6), (4, 300, 2)])
+def test_expert_backward_weight_scales_do_not_matter(bits, T, E, gu, down, mode):
+    """Steps from about 2^-15 to 2^10, gate and up apart from down: the inner
+    gradients keep their bits and stay finite.  x undoes gate's scale, so that
+    g keeps its size."""
+    c = _Case(bits, T, 2, 256, 128, E, True, 46)
+
+    def change(s, d):
+        s[:], d[:] = np.ldexp(s, gu), np.ldexp(d, down)
+        assert np.isfinite(s).all() and np.isfinite(d).all()
+    _rescale(c, change)
+    c.x *= np.float32(2.0 ** -gu)
+    dx, dw = c.run(F32, F32, F32, mode)
+    assert M.moe_device_error() == 0
+    _check_weights(c, dx, dw, mode)
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_expert_backward_one_large_block_of_weights(mode):
+    """A block of 32 weights 2^8 times the others, in up and in down."""
+    c = _Case(4, 40, 2, 256, 128, 6, True, 47)
+
+    def change(s, d):
+        s[c.H * c.I // 32 + 77] *= 256
+        d[99] *= 256
+    _rescale(c, change)
+    dx, dw = c.run(M.MOE_Q8, F32, F32, mode)
+    assert M.moe_device_error() == 0
+    _check_weights(c, dx, dw, mode)
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+def test_expert_backward_reports_weights_beyond_fp16(bits):
+    """A step whose lowest code's weight is outside fp16: exact on CUDA cores,
+    reported by the tensor cores' form, which keeps it to its expert."""
+    c = _Case(bits, 20, 2, 128, 128, 6, False, 48)
+    c.x *= np.float32(1e-6)
+    top = np.float16(65504 / 2 ** (bits - 1))              # the largest that is inside
+    for step, bad in ((top, False), (np.nextafter(top, np.float16(np.inf)), True)):
+        s, _ = _steps(c, c.blobs[3])
+        s[5] = -step
+        c.layer = M.MoELayer(bits, 128, 128, 6, 2, c.blobs, None)
+        dx, dw = c.run(F32, F32, F32, M.MOE_MODE_GEMV)
+        assert M.moe_device_error() == 0
+        _check_weights(c, dx, dw, M.MOE_MODE_GEMV)
+        dx, dw = c.run(F32, F32, F32, M.MOE_MODE_GEMM)
+        assert M.moe_device_error() == (M.DEVERR_NONFINITE if bad else 0)
+        others = _dev((c.ids != 3).all(1))
+        assert torch.isfinite(dx[others]).all() and torch.isfinite(dw[_dev(c.ids != 3)]).all()
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_expert_backward_one_large_value_a_token(mode):
+    """Each token's x and dy have one value 2^10 times the others."""
+    c = _Case(4, 40, 2, 2048, 128, 6, True, 49, sigma=0.02)
+    c.x[:, 5] *= 1024
+    c.dy[:, 1900] *= 1024
+    dx, dw = c.run(F32, F32, F32, mode)
+    assert M.moe_device_error() == 0
+    _check_weights(c, dx, dw, mode)
