@@ -1,15 +1,17 @@
 """GPU checks of the training calls at the edges of what their header allows:
-where buffers start, the range of the weights, rows that nobody computes."""
+where buffers start, rows that nobody computes, the range of the weights, a
+router with a bias, refused steps."""
 import numpy as np
 import pytest
 
+import workloads as W
 from tests import train_ref as R
 
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 import quantized_expert_ffn_route_b200 as M  # noqa: E402
-from tests.test_gpu_train import BF16, F32, MODES, _Case, _dev, _guarded, _router_case  # noqa: E402
+from tests.test_gpu_train import BF16, F32, MODES, _Case, _dev, _router_case  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -268,3 +270,98 @@ def test_expert_backward_one_large_value_a_token(mode):
     dx, dw = c.run(F32, F32, F32, mode)
     assert M.moe_device_error() == 0
     _check_weights(c, dx, dw, mode)
+
+
+# ----------------------------------------------------------------- TrainStep
+@pytest.mark.parametrize("wdt,E,T", [("bf16", 22, 37), ("f32", 22, 37), ("bf16", 24, 37), ("bf16", 13, 3)])
+def test_train_step_with_a_router_bias(wdt, E, T):
+    """A router with a bias, E a multiple of 8 and not: logits, losses and every
+    gradient against the 64-bit chain on the same routing and checkpoint."""
+    H, I, k = 256, 128, 3
+    rng = np.random.default_rng(E + T)
+    bias = rng.standard_normal(E).astype(np.float32)
+    lay = W.make_layer(9, 4, H, I, E, k, shared=True, w_dtype=wdt, bias=bias)
+    g = M.MoELayer(4, H, I, E, k, lay.blobs, lay.shared, lay.w_router, wdt, bias)
+    x = W.bf16_bits_to_f32(W.make_tokens(8, T, H, "bf16")).astype(np.float32)
+    dy = rng.standard_normal((T, H)).astype(np.float32)
+    mask = np.arange(T) % 3 != 1
+    dy[~mask] = 0
+    b, z, dl = 0.5, 0.01, -1.5
+    step = M.TrainStep(g, T, BF16, dy_dtype=F32, dx_dtype=F32, balance_coef=b, z_coef=z)
+    _, loss = step.forward(_dev(x).bfloat16(), token_mask=_dev(mask))
+    out = step.backward(_dev(dy), d_loss=torch.tensor([dl], device="cuda"))
+    torch.cuda.synchronize()
+    assert M.moe_device_error() == 0
+    wr = (W.bf16_bits_to_f32(lay.w_router) if wdt == "bf16" else lay.w_router).astype(np.float64)
+    logits = step.bufs.logits[:T * E].cpu().numpy().reshape(T, E)
+    # a sum of H products and the bias in fp32, a tensor core cutting instead of rounding
+    size = np.abs(x.astype(np.float64)) @ np.abs(wr).T + np.abs(bias)
+    assert (np.abs(logits - (x.astype(np.float64) @ wr.T + bias)) <= 2 * (H + 4) * R.U32 * size).all()
+    ids = step.bufs.ids[:T * k].cpu().numpy().reshape(T, k)
+    w = step.bufs.w[:T * k].cpu().numpy().reshape(T, k)
+    counts, losses, lgrad = R.balance(logits, ids, mask, E, b, z)
+    assert np.array_equal(step.counts.cpu().numpy(), counts)
+    # each term is a mean of positive numbers: sums of E or T fp32 terms, exponentials of differences up to
+    # `spread`; the square's factor twice its own, lse below max|l| + log E
+    per = (R.spread(logits, mask) + E + T + 24) * R.U32
+    lim = 4 * per * np.array([b * losses[1] + z * losses[2] + z, losses[1], losses[2] + 1])
+    assert (np.abs(loss.double().cpu().numpy() - losses)[:3] <= lim).all() and loss[3] == losses[3]
+    xv = R.act8(x)[2]
+    dx, dw, ex, ew = R.experts_backward(4, H, I, lay.blobs, lay.shared, ids, w, xv, dy.astype(np.float64),
+                                        R.U16 if T > 4 else 0.0)
+    want = dl * lgrad + R.gates(ids, w, dw, E, mask)
+    # d_logits: the gates' error through dw, fp32 noise of both terms, the rounding to its type
+    bound = np.zeros((T, E))
+    for t in np.nonzero(mask)[0]:
+        np.add.at(bound[t], ids[t], w[t] * (ew[t] + (w[t] * ew[t]).sum()) +
+                  (k + 8) * R.U32 * w[t] * (np.abs(dw[t]) + np.abs(w[t] * dw[t]).sum()))
+    N = mask.sum()
+    f = counts[:E] / (N * k)
+    p = np.exp(logits.astype(np.float64) - logits.max(1, keepdims=True))
+    p = np.where(mask[:, None], p / p.sum(1, keepdims=True), 0)
+    top = np.abs(logits).max() + np.log(E)
+    bound += abs(dl) * p * (b * E / N * (f + (f * p).sum(1, keepdims=True)) + z * 2 / N * top) * 2 * per
+    half = R.UBF if wdt == "bf16" else R.U32
+    gdl = step.d_logits.double().cpu().numpy()
+    assert (np.abs(gdl - want) <= bound + half * 1.01 * np.abs(want) + 1e-37).all()
+    assert (gdl[~mask] == 0).all()
+    # the router's products of the d_logits it was given: fp32 sums, cut or rounded, and the result's rounding
+    def close(got, want, size, terms, half):
+        lim = 2 * (terms + 4) * R.U32 * size
+        err = np.abs(got.double().cpu().numpy() - want)
+        assert (err <= lim + half * 1.01 * (np.abs(want) + lim) + 1e-37).all(), (err / (lim + 1e-37)).max()
+    close(out["d_w_router"], gdl.T @ xv, np.abs(gdl).T @ np.abs(xv), T, half)
+    close(out["d_bias"], gdl.sum(0), np.abs(gdl).sum(0), T, R.U32)
+    got = out["dx"].double().cpu().numpy()
+    lim = 2 * (E + 4) * R.U32 * (np.abs(gdl) @ np.abs(wr) + np.abs(dx) + ex)
+    assert (np.abs(got - (dx + gdl @ wr)) <= ex + lim + 1e-37).all()
+
+
+def test_train_step_refuses_before_it_launches_and_recovers():
+    """A refused forward() leaves the layer's buffers as they were and no
+    backward(); the next whole forward() has one again."""
+    H, I, E, k, T = 256, 128, 16, 2, 8
+    lay = W.make_layer(5, 4, H, I, E, k, shared=False, w_dtype="bf16")
+    g = M.MoELayer(4, H, I, E, k, lay.blobs, None, lay.w_router, "bf16")
+    step = M.TrainStep(g, T, BF16)
+    x, dy = torch.randn(T, H, device="cuda").bfloat16(), torch.randn(T, H, device="cuda")
+    step.forward(x)
+    want = [v.clone() for v in step.backward(dy).values()]
+    logits = step.bufs.logits.clone()
+    launches = M.moe_kernel_launches()
+    for bad in (x[:T - 1], x.float(), x.cpu(), x.t().contiguous().t(), x.float().cpu().numpy()):
+        with pytest.raises((ValueError, TypeError)):
+            step.forward(bad)
+        with pytest.raises(RuntimeError, match="forward"):
+            step.backward(dy)
+    with pytest.raises(ValueError):
+        step.forward(x, token_mask=torch.ones(T - 1, dtype=torch.bool, device="cuda"))
+    assert M.moe_kernel_launches() == launches
+    step.forward(x)
+    with pytest.raises(ValueError):
+        step.backward(dy.bfloat16())
+    with pytest.raises(ValueError):
+        step.backward(dy, d_loss=torch.ones(1))
+    assert torch.equal(step.bufs.logits, logits)
+    assert all(torch.equal(a, b) for a, b in zip(step.backward(dy).values(), want))
+    assert M.moe_device_error() == 0
