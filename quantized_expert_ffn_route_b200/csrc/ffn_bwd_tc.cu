@@ -20,10 +20,10 @@
 // token) hold them in fp16's range whatever the weights are: with D the largest
 // magnitude of a code,
 //   |u'|, |a'| <= D max|step of Wg, Wu| |x'|_1,   |q'| <= D max|step of Wd| |dy'|_1,
-// each factor is taken up to a power of two, c r times their product is 2^15,
-// and |s + a (1 - s)| < 1.1.  So none is infinite, and one that is 2^-29 of the
-// bound still has all its bits: for random weights of one size values lie
-// about 2^13 to 2^15 below it.  The steps' largest are read ahead, with the
+// the weights' part and the rows' are taken up to a power of two, c r times
+// these is 2^15, and |s + a (1 - s)| < 1.1.  So none is infinite, and one that is
+// 2^-27 of the bound still has all its bits: for random weights of one size
+// values lie about 2^13 to 2^15 below it.  The steps' largest are read ahead, with the
 // rows: a sixteenth of a weight a byte (4 bits: 1/9 of the weights' bytes).
 // They lie transposed between the phases, [2I] x rows, a group's rows padded
 // to 16: a thread of phase 1 holds one i and 16 rows, 32 bytes to store, and
@@ -257,7 +257,7 @@ __device__ __forceinline__ void block_words(const Codes<BITS> &c, __half d, uint
 }
 
 // e with c = 2^e of a group's inner gradients (a warp's call): 15 less the
-// exponents of the bound's two factors.  0 where no bound is to be had (a step
+// exponent of the weights' part of the bound.  0 where no bound is to be had (a step
 // that is infinite or NaN) or none is needed (all steps of a side are 0).
 template <int BITS>
 __device__ __forceinline__ int group_exponent(const TcArgs &p, int g) {
@@ -266,10 +266,9 @@ __device__ __forceinline__ int group_exponent(const TcArgs &p, int g) {
     const uint32_t gu = __reduce_max_sync(0xffffffffu, lane < 16 ? v : 0u);
     const uint32_t d = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : v);
     if (gu == 0u || d == 0u || gu >= 0x7C00u || d >= 0x7C00u) return 0;
-    auto up = [](uint32_t h) {                    // the smallest e with the step below 2^e
-        return static_cast<int>(__float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h)))) >> 23) - 126;
-    };
-    return 15 - 2 * (BITS - 1) - up(gu) - up(d);
+    const float both = __half2float(__ushort_as_half(static_cast<unsigned short>(gu))) *
+                       __half2float(__ushort_as_half(static_cast<unsigned short>(d)));     // exact, 2^-48 to 2^32
+    return 15 - 2 * (BITS - 1) - (static_cast<int>(__float_as_uint(both) >> 23) - 126);
 }
 __device__ __forceinline__ float exp2_of(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
@@ -777,12 +776,11 @@ __device__ __forceinline__ float2 row_scale(uint32_t top) {
     return make_float2(__uint_as_float((254u - e) << 23), __uint_as_float(e << 23));
 }
 
-// e with the sum of the scaled row's |values| below 2^e (its largest is in
-// [1, 2), but for the ends of the range), from the plain row's sum and scale:
-// 15 covers H = 8192 where the plain sum is beyond fp32.  0 for a row of zeros.
-__device__ __forceinline__ int sum_exponent(float sum, float scale) {
-    const int s = static_cast<int>(__float_as_uint(sum) >> 23), e = static_cast<int>(__float_as_uint(scale) >> 23);
-    return s >= 255 ? 15 : min(max(s + 1 - e, 0), 15);
+// The sum of the scaled row's |values| (its largest is in [1, 2), but for the
+// ends of the range) from the plain row's; 2^15 covers H = 8192 where the plain
+// sum is beyond fp32.  Nothing below 1, for rows of next to nothing.
+__device__ __forceinline__ float scaled_sum(float sum, float inv_scale) {
+    return fminf(fmaxf(sum * inv_scale, 1.f), 32768.f);
 }
 
 // Tiles of a group of n rows: as few as hold it, of equal size (a multiple of
@@ -947,14 +945,15 @@ __global__ void __launch_bounds__(kPrepThreads, V <= 2 ? 7 : 1) k_bwd_prepare(Ff
         }
     }
     if (tid == 0) {
-        int e = 0;
+        float both = 1.f;                                     // the two sums' product
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < kPrepThreads / 32; ++w) s += part_sum[which][w];
-            if (top[which] < 0x7F800000u) e += sum_exponent(s, scale[which].y);
+            if (top[which] < 0x7F800000u) both *= scaled_sum(s, scale[which].x);
         }
+        const int e = static_cast<int>(__float_as_uint(both) >> 23) - 126;     // the product is below 2^e
         p.scale[t] = make_float4(scale[0].y, scale[1].y, exp2_of(-e), exp2_of(e));
     }
 }

@@ -179,33 +179,58 @@ def _rescale(c, change):
     c.layer = M.MoELayer(c.bits, c.H, c.I, c.E, c.k, c.blobs, c.shared)
 
 
+def _g_noise(c, ua):
+    """Expected squares of the norms of dx's and d_topk_w's errors that g's own
+    error makes.  g_i sums x_h W_ih, both factors rounded: off by
+    2^0.5 ua (sum_h (x_h W_ih)^2)^0.5, independently for each i.  To first order
+    dg_i is off by q u F' of that, F = s + a (1 - s), F' = s (1 - s) (2 + g (1 - 2 s)),
+    du_i by q F and <q, a u> by q u F; dx sums them over rows of Wg and Wu.  At
+    |g| about 1 this is one of the ten roundings below; it grows with |g|."""
+    ex2, ew2 = 0.0, 0.0
+    for e in range(c.E + (c.shared is not None)):
+        Wg, Wu, Wd = R.matrices(c.bits, c.H, c.I, c.blobs[e] if e < c.E else c.shared)
+        t, j = np.nonzero(c.ids == e) if e < c.E else (np.arange(c.T), None)
+        x, w = c.xv[t], (c.w[t, j].astype(np.float64) if e < c.E else np.ones(c.T))[:, None]
+        g, u, q = x @ Wg.T, x @ Wu.T, c.dyv[t] @ Wd
+        s = 1 / (1 + np.exp(-g))
+        F, dF = s + g * s * (1 - s), s * (1 - s) * (2 + g * (1 - 2 * s))
+        var = 2 * ua * ua * ((x * x) @ (Wg * Wg).T)
+        size = np.abs(q * u * dF) * np.linalg.norm(Wg, axis=1) + np.abs(q * F) * np.linalg.norm(Wu, axis=1)
+        ex2 += (w * w * size * size * var).sum()
+        ew2 += (q * u * F * q * u * F * var).sum() if e < c.E else 0.0
+    return ex2, ew2
+
+
 def _check_weights(c, dx, dw, mode):
     """c.check with one more term.  The gradients of g and u are stored in fp16
-    times a power of two 2^15 / B' with B' at most 16 times their bound
-    B = half^2 max|step of gate, up| max|step of down| |x|_1 |dy|_1 (four factors,
-    each taken up to a power of two).  fp16's smallest step is 2^-24: a stored
-    value is off by up to 2^-25 2^-15 16 B = 2^-36 B."""
+    times a power of two 2^15 / B' with B' at most 4 times their bound
+    B = half^2 max|step of gate, up| max|step of down| |x|_1 |dy|_1 (the weights'
+    part and the rows', each taken up to a power of two).  fp16's smallest step
+    is 2^-24: a stored value is off by up to 2^-25 2^-15 4 B = 2^-38 B."""
     gemm = mode == M.MOE_MODE_GEMM
     rx, rw, ex, ew = R.experts_backward(c.bits, c.H, c.I, c.blobs, c.shared, c.ids, c.w, c.xv, c.dyv,
                                         R.U16 if gemm else 0.0)
+    lost = 0.0                                             # the same for dx's norm, each i apart
     if gemm:
         l1 = np.abs(c.xv).sum(1) * np.abs(c.dyv).sum(1)
         for e in range(c.E + (c.shared is not None)):
             blob = c.blobs[e] if e < c.E else c.shared
             gu, d = (float(np.abs(s.astype(np.float64)).max()) for s in _steps(c, blob))
-            floor = 2.0 ** -36 * 4.0 ** (c.bits - 1) * gu * d * l1
+            floor = 2.0 ** -38 * 4.0 ** (c.bits - 1) * gu * d * l1
             Wg, Wu, _ = R.matrices(c.bits, c.H, c.I, blob)
             col = np.abs(Wg).sum(0) + np.abs(Wu).sum(0)
             wt = np.where(c.ids == e, c.w, 0).sum(1) if e < c.E else 1.0
             ex = ex + 1.1 * (wt * floor)[:, None] * col
+            lost += ((wt * floor) ** 2).sum() * ((Wg * Wg).sum() + (Wu * Wu).sum())
     gx, gw = dx.double().cpu().numpy(), dw.double().cpu().numpy()
     assert np.isfinite(gx).all() and np.isfinite(gw).all()
     assert (np.abs(gx - rx) <= ex + 1e-37).all(), (np.abs(gx - rx) / (ex + 1e-37)).max()
     assert (np.abs(gw - rw) <= ew + 1e-37).all(), (np.abs(gw - rw) / (ew + 1e-37)).max()
-    # as in c.check: about ten independent roundings of half a step along a value's path
-    rms = np.sqrt(10.0) * (R.U16 if gemm else 32 * R.U32)
-    assert np.linalg.norm(gx - rx) <= rms * np.linalg.norm(rx)
-    assert np.linalg.norm(gw - rw) <= rms * np.linalg.norm(rw)
+    # as in c.check: about ten independent roundings of half a step along a value's path; and g's, and the
+    # smallest steps
+    half = R.U16 if gemm else 32 * R.U32
+    for err, size, g2, l2 in zip((gx - rx, gw - rw), (rx, rw), _g_noise(c, half), (lost, 0.0)):
+        assert (err ** 2).sum() <= 10 * half ** 2 * (size ** 2).sum() + g2 + l2
 
 
 @pytest.mark.parametrize("mode", MODES)
@@ -259,6 +284,24 @@ def test_expert_backward_reports_weights_beyond_fp16(bits):
         assert M.moe_device_error() == (M.DEVERR_NONFINITE if bad else 0)
         others = _dev((c.ids != 3).all(1))
         assert torch.isfinite(dx[others]).all() and torch.isfinite(dw[_dev(c.ids != 3)]).all()
+
+
+@pytest.mark.parametrize("side", ["up", "down"])
+def test_expert_backward_largest_steps_at_the_end(side):
+    """Matrices whose steps take a block several rounds to look through, the
+    large ones (2^14 times the others) in the last rows: missed, they would
+    take the inner gradients past fp16's end."""
+    c = _Case(4, 6, 1, 4096, 1536, 2, False, 50, sigma=0.02)
+
+    def change(s, d):
+        t = s if side == "up" else d
+        n = c.H * c.I // 32 // 16
+        t[-n:] = np.ldexp(t[-n:], 14)
+        assert np.isfinite(t).all()
+    _rescale(c, change)
+    dx, dw = c.run(M.MOE_Q8, BF16, F32, M.MOE_MODE_GEMM)
+    assert M.moe_device_error() == 0
+    _check_weights(c, dx, dw, M.MOE_MODE_GEMM)
 
 
 @pytest.mark.parametrize("mode", MODES)
