@@ -56,7 +56,7 @@
 // of 128 rows (phase 1) leaves room for three B stages and fills TMEM with its
 // accumulators and A (96 rows and three A stages: 862 us); of 256 (phase 2) reads
 // the weights least (192: 564 us for 526, 128: 605).  The gather moves its 770 MB
-// at 5.5 TB/s.  At 16 tokens (phases 103 and 72) the transposed tile's warps take
+// at 5.5 TB/s.  At 16 tokens (phases 94 and 67 at 2 bits) the transposed tile's warps take
 // longest; twice as many of them gained 4 us there and cost 80 at 8192, in
 // registers.
 #include "common.cuh"
