@@ -99,12 +99,16 @@ int moe_route_backward(const float *logits, const int32_t *topk_ids, const float
 // ---------------------------------------------------------------- experts
 // Up to four tokens on CUDA cores: a group has a row or two then, and the tensor
 // cores' form pays three launches' latencies and tiles of 64 rows.  Measured as
-// graphs, CUDA cores against tensor cores (2048 x 512, 4 bits): top-10 of 512,
-// 28 : 47 us at one token, 72 : 84 at 4, 108 : 97 at 6; top-4 of 64, 21 : 41,
-// 34 : 47, 48 : 50; at 4096 x 1536, top-4 of 32, 52 : 75, 139 : 106, 196 : 173.
-// So the rule is a compromise: rows an expert and bytes of a blob decide, not
-// tokens (larger experts would cross over at 2 to 4 tokens, the smallest step at
-// 6), and 2 bits, for which it holds too, were not measured.
+// graphs with a shared expert, us on CUDA cores : on tensor cores, 4 bits | 2 bits:
+//                              1 token         4 tokens          6 tokens         16 tokens
+//   2048 x 512, top-10 of 512  29:46 | 29:45    73:82 | 67:77   108:96 | 96:88    247:183 | 231:171
+//   2048 x 512, top-4 of 64    21:40 | 20:38    34:45 | 34:44    48:49 | 48:47    111:57  | 107:53
+//   4096 x 1536, top-4 of 32   58:83 | 57:80   153:149 | 141:135 225:169 | 211:154 481:245 | 465:229
+// Rows an expert and a blob's bytes move the crossing by a token or two; nowhere
+// here does the rule cost more than 4 %.  From five tokens on the operands are
+// thereby rounded to fp16, as the forward pass's are in its GEMM mode; fp32
+// throughout at 16 tokens would take 1.3 to 2 times as long, and MOE_MODE_GEMV
+// asks for it.
 static int backward_mode(int mode, int T) {
     if (mode == MOE_MODE_AUTO) return T <= 4 ? MOE_MODE_GEMV : MOE_MODE_GEMM;
     return mode;
